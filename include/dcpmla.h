@@ -464,6 +464,169 @@ int pcp_prefill_attention(const void* q, const int32_t* positions, int num_queri
                           float* out_lse, void* workspace, size_t workspace_bytes,
                           int num_splits, int impl, void* stream);
 
+/*
+ * Block summaries: what a cheap score needs of every 64-row cache block.
+ *
+ * A summary is the mean of the block's rows (576 values, rope included) as
+ * int8 codes, 608 bytes: 576 codes, 5 fp32 scales (latent groups of 128 values,
+ * then the 64 rope values), 12 bytes of zeros.  Per group scale = max|mean| /
+ * 127 (1 if that is 0), code = mean / scale rounded to nearest even; a mean
+ * that is not finite counts as 0.  The pages have no counterpart to this call.
+ *
+ *   summaries        [num_blocks][608], 16-byte aligned: the summary of cache
+ *                    block k is entry k.
+ *   seq_lens         [batch] int32 GLOBAL lengths, as in mla_decode_partial.
+ *   first_positions  NULL: every block of every request is summarised.  Else
+ *                    [batch] int32 global positions: only the blocks that hold
+ *                    a row of this shard at or past them (after a decode step:
+ *                    the position of its first new token).  Nothing else of
+ *                    `summaries` is written.
+ *   flags            NULL or a DEVICE int32: DCPMLA_FLAG_BAD_BLOCK,
+ *                    DCPMLA_FLAG_BAD_LENGTH; such blocks are skipped.
+ * Rows past a request's end do not enter the mean, whatever they hold.  A block
+ * that several requests share should be full or of one length in all of them:
+ * else its summary is that of any one of them.
+ * Returns DCPMLA_OK or a negative code.
+ */
+#define DCPMLA_SUMMARY_BYTES 608
+int mla_block_summary(const void* kv_cache, int kv_dtype, int64_t num_blocks, int block_size,
+                      const int32_t* block_table, int block_table_stride, const int32_t* seq_lens,
+                      const int32_t* first_positions, int batch, int shard_id, int num_shards,
+                      void* summaries, int32_t* flags, void* stream);
+
+/*
+ * The blocks of this shard that each query token reads, by the summaries.
+ *
+ * Per head and group the query is held as int8 codes too (step = max|q| / 127,
+ * 1 if that is 0; values that are not finite count as 0), and with the code
+ * products dot_g (whole numbers)
+ *     s_hb   = sum over groups, in order, of fp32(dot_g) * (step_hg * scale_bg)
+ *     rank_b = max_h (s_hb - max_b' s_hb')
+ * in fp32, each operation rounded by itself.  Taken are the first sink_blocks
+ * and the last recent_blocks of the request's blocks on this shard, then the
+ * highest ranks, ties to the lowest index, block_topk in all (all of them if
+ * there are no more).  The choice does not depend on launch shapes.
+ *
+ *   q           [batch][q_len][num_heads][576] bf16, 16-byte aligned; query i
+ *               of request b sees the positions up to L_b - q_len + i.  num_heads
+ *               1..64, q_len 1..64, batch * q_len <= 65,535.
+ *   block_topk  >= sink_blocks + recent_blocks, recent_blocks >= 1 (the last
+ *               block, which may be partly filled, is always taken).
+ *   block_table_stride  at most 393,216 (else DCPMLA_ERR_UNSUPPORTED).
+ *   out_blocks  NULL or [batch][q_len][block_topk] int32: the blocks taken, as
+ *               indices of the request's blocks, ascending, then -1.
+ *   out_table   [batch][q_len][block_topk] int32: the same blocks' table
+ *               entries, then -1: with out_lens, a table that
+ *               mla_decode_partial reads as one shard of batch * q_len requests
+ *               (shard_id 0, num_shards 1).
+ *   out_lens    [batch][q_len] int32: rows in the blocks taken.
+ *   workspace   mla_block_select_workspace_size(...) bytes, 16-byte aligned;
+ *               its flag word as in mla_decode_workspace_size.
+ * A table entry outside the pool is flagged and ranks last.
+ * Returns DCPMLA_OK or a negative code.
+ */
+int mla_block_select_workspace_size(int batch, int num_heads, int q_len, int block_table_stride,
+                                    size_t* bytes);
+int mla_block_select(const void* q, const void* summaries, int64_t num_blocks, int block_size,
+                     const int32_t* block_table, int block_table_stride, const int32_t* seq_lens,
+                     int batch, int num_heads, int q_len, int shard_id, int num_shards,
+                     int block_topk, int sink_blocks, int recent_blocks, int32_t* out_blocks,
+                     int32_t* out_table, int32_t* out_lens, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * Block-sparse decode of one shard: mla_block_select, then mla_decode_partial
+ * over the blocks taken (every query token over its own).  Arguments as in
+ * those two calls (out_partial [batch][q_len][num_heads][512], out_lse
+ * [batch][q_len][num_heads], out_blocks may be NULL); the partials of the
+ * shards merge with dcp_merge.  impl is one of DCPMLA_IMPL_* (the test bit is
+ * refused).  With block_topk at least the number of blocks this is dense
+ * decode.  The flag word is the workspace's first.
+ * Returns DCPMLA_OK or a negative code.
+ */
+int mla_decode_blocks_workspace_size(int batch, int num_heads, int q_len, int block_table_stride,
+                                     int block_topk, int num_splits, size_t* bytes);
+int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const void* summaries,
+                      int64_t num_blocks, int block_size, const int32_t* block_table,
+                      int block_table_stride, const int32_t* seq_lens, int batch, int num_heads,
+                      int q_len, int shard_id, int num_shards, int block_topk, int sink_blocks,
+                      int recent_blocks, float softmax_scale, float* out_partial, float* out_lse,
+                      int32_t* out_blocks, void* workspace, size_t workspace_bytes,
+                      int num_splits, int impl, void* stream);
+
+/*
+ * Accumulated attention weight of this shard's cached rows:
+ *     mass[b][j] = decay * mass[b][j] + sum_{i,h} exp(scale * <q_bih, k_bj> - lse_bih)
+ * for every local row j, where query i of request b counts for the rows at
+ * positions up to L_b - q_len + i.  Under DCP `lse` is the merged LSE of all
+ * shards, so that a row's weight is its share of the whole attention.
+ *
+ *   q            [batch][q_len][num_heads][576] bf16, 16-byte aligned; num_heads
+ *                1..64, q_len 1..64.  64 / num_heads queries run in one pass over
+ *                the cache; more queries take more passes.
+ *   lse          [batch][q_len][num_heads] fp32 natural-log LSE (-inf: the query
+ *                saw nothing and adds nothing).
+ *   decay        finite, >= 0; 0: the old mass is not read (it may be anything).
+ *   mass         [batch][mass_stride] fp32, in local row order; nothing past a
+ *                request's rows is touched.  Rows beyond mass_stride are flagged
+ *                (DCPMLA_FLAG_BAD_LENGTH) and skipped; so are the rows of table
+ *                entries outside the pool (DCPMLA_FLAG_BAD_BLOCK).
+ *   workspace    mla_attention_mass_workspace_size(...) bytes, 16-byte aligned;
+ *                its flag word as in mla_decode_workspace_size.
+ *   num_splits   CTAs (0: the SM count).
+ * The result does not depend on num_splits.
+ * Returns DCPMLA_OK or a negative code.
+ */
+int mla_attention_mass_workspace_size(int batch, int num_heads, int q_len, size_t* bytes);
+int mla_attention_mass(const void* q, const void* kv_cache, int kv_dtype, int64_t num_blocks,
+                       int block_size, const int32_t* block_table, int block_table_stride,
+                       const int32_t* seq_lens, int batch, int num_heads, int q_len, int shard_id,
+                       int num_shards, float softmax_scale, const float* lse, float decay,
+                       float* mass, int64_t mass_stride, void* workspace, size_t workspace_bytes,
+                       int num_splits, void* stream);
+
+/*
+ * Eviction by accumulated weight: of each request's rows on this shard the
+ * `budget` with the largest mass stay, in place.
+ *
+ * Rows at positions t < sink or t >= L_b - recent come before all others (sink
+ * + recent <= budget), then larger mass, then the lower row; a NaN mass is the
+ * smallest.  A request of at most `budget` rows keeps all.  A kept row below
+ * the budget stays where it is; the kept rows at or past it fill, in order, the
+ * places below it that were given up.  Rows 0 .. rows_out[b]-1 are then the
+ * request's cache; the blocks past them are free.  Attention does not depend on
+ * the order of the rows, but they are no longer in token order: decode them as
+ * one shard of their own (shard_id 0, num_shards 1, seq_lens = rows_out), and
+ * append at local row rows_out[b] in the same way.
+ *
+ *   seq_lens      [batch] int32 GLOBAL lengths L_b (for `recent`).
+ *   rows          NULL before the first eviction (the shard's share of L_b), else
+ *                 [batch] int32 rows held.
+ *   mass          [batch][mass_stride] fp32.
+ *   positions     NULL before the first eviction (row j is token j * num_shards
+ *                 + shard_id), else [batch][mass_stride] int32 token of each row.
+ *   mass_out, positions_out  the kept rows' entries in their new order, the rest
+ *                 untouched; each may be the input array itself (no other
+ *                 overlap).  positions_out may be NULL.
+ *   rows_out      [batch] int32, not `rows`.
+ *   kv_cache      rows are moved within each request's blocks: no block written
+ *                 to may be shared with another request.
+ *   workspace     mla_cache_evict_workspace_size(...) bytes, 16-byte aligned; its
+ *                 flag word as in mla_decode_workspace_size.  A length or row
+ *                 count beyond the table row or mass_stride is clipped and
+ *                 flagged (DCPMLA_FLAG_BAD_LENGTH); a row whose table entry is
+ *                 outside the pool is flagged and not copied.
+ * At most 8,388,608 rows a request (else DCPMLA_ERR_UNSUPPORTED); batch <=
+ * 65,535.  Returns DCPMLA_OK or a negative code.
+ */
+int mla_cache_evict_workspace_size(int batch, int budget, size_t* bytes);
+int mla_cache_evict(void* kv_cache, int kv_dtype, int64_t num_blocks, int block_size,
+                    const int32_t* block_table, int block_table_stride, const int32_t* seq_lens,
+                    const int32_t* rows, int batch, int shard_id, int num_shards,
+                    const float* mass, const int32_t* positions, int64_t mass_stride, int budget,
+                    int sink, int recent, float* mass_out, int32_t* positions_out,
+                    int32_t* rows_out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a return code (never NULL). */
 const char* dcpmla_error_string(int code);
 

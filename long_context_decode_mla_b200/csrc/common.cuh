@@ -24,6 +24,8 @@ constexpr int kRowBytesFp8 = 656;
 // (64 rows x 128 B), each in the kernel's 128-byte-swizzled shared-memory
 // order, then the 64 per-head frame factors 2^-a (fp32).
 constexpr int kQImageBytes = 2 * 4 * 8192 + 8192 + 64 * 4;
+// Summary of one cache block: 576 int8 codes, 5 fp32 scales, 12 bytes of zeros.
+constexpr int kSummaryBytes = 608;
 constexpr int kWsHeader = 256;    // workspace header: flag word + reserved
 constexpr int kMaxDevicesConfigured = 64;   // device ordinals the per-device caches cover
 

@@ -82,6 +82,29 @@ def lib() -> ctypes.CDLL:
     L.pcp_prefill_attention.argtypes = [vp, vp, i32, i32, vp, i32, i64, f32, vp, vp, vp, sz, i32,
                                         i32, vp]
     L.pcp_prefill_attention.restype = i32
+    szp = ctypes.POINTER(sz)
+    L.mla_block_summary.argtypes = [vp, i32, i64, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp]
+    L.mla_block_summary.restype = i32
+    L.mla_block_select_workspace_size.argtypes = [i32, i32, i32, i32, szp]
+    L.mla_block_select_workspace_size.restype = i32
+    L.mla_block_select.argtypes = [vp, vp, i64, i32, vp, i32, vp, i32, i32, i32, i32, i32, i32,
+                                   i32, i32, vp, vp, vp, vp, sz, vp]
+    L.mla_block_select.restype = i32
+    L.mla_decode_blocks_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, szp]
+    L.mla_decode_blocks_workspace_size.restype = i32
+    L.mla_decode_blocks.argtypes = [vp, vp, i32, vp, i64, i32, vp, i32, vp, i32, i32, i32, i32,
+                                    i32, i32, i32, i32, f32, vp, vp, vp, vp, sz, i32, i32, vp]
+    L.mla_decode_blocks.restype = i32
+    L.mla_attention_mass_workspace_size.argtypes = [i32, i32, i32, szp]
+    L.mla_attention_mass_workspace_size.restype = i32
+    L.mla_attention_mass.argtypes = [vp, vp, i32, i64, i32, vp, i32, vp, i32, i32, i32, i32, i32,
+                                     f32, vp, f32, vp, i64, vp, sz, i32, vp]
+    L.mla_attention_mass.restype = i32
+    L.mla_cache_evict_workspace_size.argtypes = [i32, i32, szp]
+    L.mla_cache_evict_workspace_size.restype = i32
+    L.mla_cache_evict.argtypes = [vp, i32, i64, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, i64,
+                                  i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.mla_cache_evict.restype = i32
     _lib = L
     return L
 
@@ -327,6 +350,204 @@ def pcp_prefill_attention(q, positions, gathered, kv_dtype, softmax_scale, out, 
     _check(rc, "pcp_prefill_attention")
 
 
+SUMMARY_BYTES = 608                       # DCPMLA_SUMMARY_BYTES
+
+
+def _kv(kv_dtype) -> int:
+    return KV_DTYPES[kv_dtype] if isinstance(kv_dtype, str) else int(kv_dtype)
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _expect(name, t, dtype, shape=None):
+    """A tensor argument that is passed on as a raw pointer: its type, shape and order."""
+    if t is None:
+        return
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+        want = f"{dtype}" + ("" if shape is None else f" {list(shape)}")
+        raise ValueError(f"{name} must be contiguous {want}, got {t.dtype} {list(t.shape)}")
+
+
+def _on_current_device(*tensors):
+    """Raw pointers go to kernels on the current device's stream: nothing else may pass."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError(f"a tensor on {t.device} was given to a call on cuda device {cur}")
+
+
+def _query_shape(q) -> tuple[int, int, int]:
+    """(batch, q_len, heads) of q [B, H, 576] or [B, q_len, H, 576]."""
+    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
+        raise ValueError(f"q must be [B, H, {HEAD_DIM}] or [B, q_len, H, {HEAD_DIM}], "
+                         f"got {list(q.shape)}")
+    _expect("q", q, torch.bfloat16)
+    return (q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2])
+
+
+def _expect_table(block_table, seq_lens, batch):
+    _expect("seq_lens", seq_lens, torch.int32, (batch,))
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, stride], got {list(block_table.shape)}")
+    _expect("block_table", block_table, torch.int32)
+
+
+def _size(fn, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _check(getattr(lib(), fn)(*args, ctypes.byref(n)), fn)
+    return n.value
+
+
+def mla_block_summary(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_shards, summaries,
+                      first_positions=None, flags=None, stream=None,
+                      block_size: int = BLOCK_SIZE, num_blocks: int | None = None):
+    """Summaries of this shard's cache blocks (see include/dcpmla.h).
+
+    block_table [B, stride] int32, seq_lens [B] int32 global lengths, summaries
+    [num_blocks, 608] uint8; ``first_positions`` [B] int32 limits the call to
+    the blocks that hold a row at or past them (the newest tokens' blocks after
+    a decode step); ``flags`` an optional one-element int32 device tensor.
+    """
+    nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    _expect_table(block_table, seq_lens, seq_lens.shape[0])
+    _expect("first_positions", first_positions, torch.int32, tuple(seq_lens.shape))
+    _expect("summaries", summaries, torch.uint8, (nb, SUMMARY_BYTES))
+    _on_current_device(kv_cache, block_table, seq_lens, first_positions, summaries, flags)
+    rc = lib().mla_block_summary(
+        _ptr(kv_cache), _kv(kv_dtype), nb, block_size, _ptr(block_table), block_table.shape[1],
+        _ptr(seq_lens), _ptr(first_positions), block_table.shape[0], shard_id, num_shards,
+        _ptr(summaries), _ptr(flags), _stream(stream))
+    _check(rc, "mla_block_summary")
+
+
+def mla_block_select_workspace_size(batch: int, num_heads: int, q_len: int,
+                                    block_table_stride: int) -> int:
+    return _size("mla_block_select_workspace_size", batch, num_heads, q_len, block_table_stride)
+
+
+def mla_block_select(q, summaries, block_table, seq_lens, shard_id, num_shards, block_topk,
+                     out_table, out_lens, workspace, out_blocks=None, sink_blocks: int = 1,
+                     recent_blocks: int = 1, stream=None, block_size: int = BLOCK_SIZE):
+    """The blocks each query token reads (see include/dcpmla.h).
+
+    q [B, H, 576] or [B, q_len, H, 576]; out_table, out_blocks
+    [B * q_len, block_topk] int32, out_lens [B * q_len] int32 (or the same
+    with [B, q_len] in front).
+    """
+    B, Q, H = _query_shape(q)
+    _expect_table(block_table, seq_lens, B)
+    _expect("summaries", summaries, torch.uint8, (summaries.shape[0], SUMMARY_BYTES))
+    for name, t, n in (("out_table", out_table, B * Q * block_topk), ("out_lens", out_lens, B * Q),
+                       ("out_blocks", out_blocks, B * Q * block_topk)):
+        _expect(name, t, torch.int32)
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must hold {n} values, got {list(t.shape)}")
+    _on_current_device(q, summaries, block_table, seq_lens, out_table, out_lens, out_blocks, workspace)
+    rc = lib().mla_block_select(
+        _ptr(q), _ptr(summaries), summaries.shape[0], block_size, _ptr(block_table),
+        block_table.shape[1], _ptr(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
+        sink_blocks, recent_blocks, _ptr(out_blocks), _ptr(out_table), _ptr(out_lens),
+        _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(rc, "mla_block_select")
+
+
+def mla_decode_blocks_workspace_size(batch: int, num_heads: int, q_len: int,
+                                     block_table_stride: int, block_topk: int,
+                                     num_splits: int = 0) -> int:
+    return _size("mla_decode_blocks_workspace_size", batch, num_heads, q_len, block_table_stride,
+                 block_topk, num_splits)
+
+
+def mla_decode_blocks(q, kv_cache, kv_dtype, summaries, block_table, seq_lens, shard_id,
+                      num_shards, block_topk, softmax_scale, out_partial, out_lse, workspace,
+                      out_blocks=None, sink_blocks: int = 1, recent_blocks: int = 1,
+                      num_splits: int = 0, impl: str | int = "auto", stream=None,
+                      block_size: int = BLOCK_SIZE, num_blocks: int | None = None):
+    """One shard's decode over the blocks its summaries rank highest (see
+    include/dcpmla.h): q [B, H, 576] or [B, q_len, H, 576]."""
+    B, Q, H = _query_shape(q)
+    nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    _expect_table(block_table, seq_lens, B)
+    _expect("summaries", summaries, torch.uint8, (nb, SUMMARY_BYTES))
+    for name, t, dtype, n in (("out_partial", out_partial, torch.float32, B * Q * H * V_DIM),
+                              ("out_lse", out_lse, torch.float32, B * Q * H),
+                              ("out_blocks", out_blocks, torch.int32, B * Q * block_topk)):
+        _expect(name, t, dtype)
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must hold {n} values, got {list(t.shape)}")
+    impl_code = IMPLS[impl] if isinstance(impl, str) else int(impl)
+    _on_current_device(q, kv_cache, summaries, block_table, seq_lens, out_partial, out_lse, out_blocks,
+                       workspace)
+    rc = lib().mla_decode_blocks(
+        _ptr(q), _ptr(kv_cache), _kv(kv_dtype), _ptr(summaries), nb, block_size, _ptr(block_table),
+        block_table.shape[1], _ptr(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
+        sink_blocks, recent_blocks, float(softmax_scale), _ptr(out_partial), _ptr(out_lse),
+        _ptr(out_blocks), _ptr(workspace), _nbytes(workspace), num_splits, impl_code,
+        _stream(stream))
+    _check(rc, "mla_decode_blocks")
+
+
+def mla_attention_mass_workspace_size(batch: int, num_heads: int, q_len: int = 1) -> int:
+    return _size("mla_attention_mass_workspace_size", batch, num_heads, q_len)
+
+
+def mla_attention_mass(q, kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_shards,
+                       softmax_scale, lse, mass, workspace, decay: float = 1.0,
+                       num_splits: int = 0, stream=None, block_size: int = BLOCK_SIZE,
+                       num_blocks: int | None = None):
+    """Adds this step's attention weight to ``mass`` [B, rows] (see
+    include/dcpmla.h): q [B, H, 576] or [B, q_len, H, 576], lse the (merged)
+    LSE of the same queries and heads."""
+    B, Q, H = _query_shape(q)
+    nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    _expect_table(block_table, seq_lens, B)
+    _expect("lse", lse, torch.float32)
+    if lse.numel() != B * Q * H:
+        raise ValueError(f"lse must hold {B * Q * H} values, got {list(lse.shape)}")
+    _expect("mass", mass, torch.float32, (B, mass.shape[-1]))
+    _on_current_device(q, kv_cache, block_table, seq_lens, lse, mass, workspace)
+    rc = lib().mla_attention_mass(
+        _ptr(q), _ptr(kv_cache), _kv(kv_dtype), nb, block_size, _ptr(block_table),
+        block_table.shape[1], _ptr(seq_lens), B, H, Q, shard_id, num_shards, float(softmax_scale),
+        _ptr(lse), float(decay), _ptr(mass), mass.shape[-1], _ptr(workspace), _nbytes(workspace),
+        num_splits, _stream(stream))
+    _check(rc, "mla_attention_mass")
+
+
+def mla_cache_evict_workspace_size(batch: int, budget: int) -> int:
+    return _size("mla_cache_evict_workspace_size", batch, budget)
+
+
+def mla_cache_evict(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_shards, mass, budget,
+                    mass_out, rows_out, workspace, rows=None, positions=None, positions_out=None,
+                    sink: int = 0, recent: int = 0, stream=None, block_size: int = BLOCK_SIZE,
+                    num_blocks: int | None = None):
+    """Keeps the ``budget`` rows of largest mass of every request, in place (see
+    include/dcpmla.h).  mass, mass_out fp32 and positions, positions_out int32
+    are [B, rows]; an output may be the input itself."""
+    B = seq_lens.shape[0]
+    nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    _expect_table(block_table, seq_lens, B)
+    shape = (B, mass.shape[-1])
+    for name, t, dtype, sh in (("mass", mass, torch.float32, shape),
+                               ("mass_out", mass_out, torch.float32, shape),
+                               ("positions", positions, torch.int32, shape),
+                               ("positions_out", positions_out, torch.int32, shape),
+                               ("rows", rows, torch.int32, (B,)),
+                               ("rows_out", rows_out, torch.int32, (B,))):
+        _expect(name, t, dtype, sh)
+    _on_current_device(kv_cache, block_table, seq_lens, rows, mass, positions, mass_out, positions_out,
+                       rows_out, workspace)
+    rc = lib().mla_cache_evict(
+        _ptr(kv_cache), _kv(kv_dtype), nb, block_size, _ptr(block_table), block_table.shape[1],
+        _ptr(seq_lens), _ptr(rows), B, shard_id, num_shards, _ptr(mass), _ptr(positions),
+        mass.shape[-1], budget, sink, recent, _ptr(mass_out), _ptr(positions_out), _ptr(rows_out),
+        _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(rc, "mla_cache_evict")
+
+
 class PcpPrefill:
     """One request's PCP prefill on one GPU: the gathered copy of its prompt
     rows and each rank's causal attention over it (the ranks of a real PCP
@@ -424,19 +645,38 @@ class DcpDecoder:
     different streams never share scratch memory.  With ``q_len`` > 1 the
     step is multi-query decode: ``prob.q`` holds [B, q_len * H, 576] rows
     ordered [q_len][H], and the outputs have q_len * H rows in that order.
+
+    With ``block_topk`` > 0 every query token reads only that many 64-row
+    blocks of each shard, picked by ``prob.block_summaries`` (kept up to date
+    with :func:`mla_block_summary`): the first ``sink_blocks``, the last
+    ``recent_blocks`` and the highest ranked.  ``max_blocks`` is the block
+    tables' stride; the blocks read are in ``blocks`` [N, B, q_len,
+    block_topk].
     """
 
     def __init__(self, batch, heads, num_shards, topk=0, num_splits=0, device="cuda",
-                 impl="auto", streams=None, q_len=1):
+                 impl="auto", streams=None, q_len=1, block_topk=0, max_blocks=0, sink_blocks=1,
+                 recent_blocks=1):
         self.batch, self.heads, self.num_shards = batch, heads, num_shards
         self.num_splits, self.impl, self.topk, self.q_len = num_splits, impl, topk, q_len
+        self.block_topk, self.sink_blocks, self.recent_blocks = block_topk, sink_blocks, recent_blocks
         rows = heads * q_len                 # multi-query: rows [q_len][heads]
         dev = torch.device(device)
         self.partials = torch.empty(num_shards, batch, rows, V_DIM, device=dev)
         self.lses = torch.empty(num_shards, batch, rows, device=dev)
         self.out = torch.empty(batch, rows, V_DIM, device=dev)
         self.out_lse = torch.empty(batch, rows, device=dev)
-        nbytes = mla_decode_workspace_size(batch, rows, num_splits, topk)
+        self.blocks = None
+        if block_topk:
+            if topk or max_blocks < 1:
+                raise ValueError("block_topk takes no topk and needs max_blocks, the block "
+                                 "tables' stride")
+            nbytes = mla_decode_blocks_workspace_size(batch, heads, q_len, max_blocks, block_topk,
+                                                      num_splits)
+            self.blocks = torch.empty(num_shards, batch, q_len, block_topk, dtype=torch.int32,
+                                      device=dev)
+        else:
+            nbytes = mla_decode_workspace_size(batch, rows, num_splits, topk)
         self.workspaces = [torch.zeros(nbytes, dtype=torch.uint8, device=dev)
                            for _ in range(num_shards)]
         self.streams = streams
@@ -459,7 +699,15 @@ class DcpDecoder:
             st = streams[s % len(streams)] if streams else base
             if streams:
                 st.wait_event(ev)
-            if self.q_len > 1:
+            if self.block_topk:
+                mla_decode_blocks(prob.q.view(self.batch, self.q_len, self.heads, HEAD_DIM),
+                                  prob.kv_cache, prob.kv_dtype, prob.block_summaries,
+                                  prob.block_tables[s], prob.seq_lens, s, self.num_shards,
+                                  self.block_topk, prob.softmax_scale, self.partials[s],
+                                  self.lses[s], self.workspaces[s], self.blocks[s],
+                                  self.sink_blocks, self.recent_blocks, self.num_splits, self.impl,
+                                  st, prob.block_size)
+            elif self.q_len > 1:
                 qv = prob.q.view(self.batch, self.q_len, self.heads, HEAD_DIM)
                 mla_decode_partial_multi(qv, prob.kv_cache, prob.kv_dtype, prob.block_tables[s],
                                          prob.seq_lens, s, self.num_shards, prob.softmax_scale,

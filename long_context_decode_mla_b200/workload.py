@@ -79,6 +79,7 @@ class DecodeProblem:
     sparse_idx: torch.Tensor | None = None   # int32 [B, topk] or None
     block_size: int = BLOCK_SIZE
     meta: dict = field(default_factory=dict)
+    block_summaries: torch.Tensor | None = None   # uint8 [num_blocks, 608] or None
 
     @property
     def batch(self) -> int:
@@ -92,7 +93,8 @@ class DecodeProblem:
         mv = lambda t: None if t is None else t.to(device)  # noqa: E731
         return DecodeProblem(mv(self.q), mv(self.kv_cache), self.kv_dtype, mv(self.block_tables),
                              mv(self.seq_lens), self.num_shards, self.softmax_scale,
-                             mv(self.sparse_idx), self.block_size, dict(self.meta))
+                             mv(self.sparse_idx), self.block_size, dict(self.meta),
+                             mv(self.block_summaries))
 
     def numpy_inputs(self) -> dict:
         """The same bytes as numpy arrays (bf16 as uint16 bit patterns)."""

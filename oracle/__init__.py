@@ -15,3 +15,4 @@ from .multi_query import dcp_decode_multi, mla_decode_partial_multi  # noqa: F40
 from .pcp import (  # noqa: F401
     gather_prompt_rows, pcp_chunks, pcp_prefill, pcp_prefill_rank, pcp_rank_tokens,
 )
+from . import block_cache  # noqa: F401
