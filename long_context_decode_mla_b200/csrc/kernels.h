@@ -1,11 +1,22 @@
 // Internal launch entry points shared between the kernel files and the C ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 
 namespace dcpmla {
+
+// cuTensorMapEncodeTiled of the driver, nullptr if it has none.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder();
+
+// Q operand images of every request into p.q_image (q_image.cuh).
+cudaError_t launch_q_image(const PartialParams& p, cudaStream_t st);
 
 cudaError_t launch_partial_simt(const PartialParams& p, int kv_dtype, cudaStream_t st);
 cudaError_t launch_partial_tc(const PartialParams& p, int kv_dtype, cudaStream_t st);

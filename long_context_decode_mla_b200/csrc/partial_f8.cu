@@ -1067,28 +1067,9 @@ __global__ void __launch_bounds__(256) f8_q_image_kernel(const PartialParams p, 
 
 // ---------------------------------------------------------------- host -----
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
 // Tensor maps over the cache pool viewed as [num_blocks][64 rows][656 bytes].
 bool encode_maps(const PartialParams& p, CUtensorMap* rows, CUtensorMap* scales) {
-  EncodeTiledFn enc = encode_fn();
+  EncodeTiledFn enc = tensor_map_encoder();
   if (!enc) return false;
   if (p.row_ids) {
     // listed rows: the cache as [blocks * 64][656] bytes, boxes one row high
@@ -1124,9 +1105,28 @@ bool g_attr_done[2][kMaxDevicesConfigured] = {};   // [listed rows][device]
 
 }  // namespace
 
+EncodeTiledFn tensor_map_encoder() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+cudaError_t launch_q_image(const PartialParams& p, cudaStream_t st) {
+  f8_q_image_kernel<<<dim3(p.batch, 2), 256, 0, st>>>(p, p.q_image);
+  return cudaGetLastError();
+}
+
 bool f8_supports(const PartialParams& p, int kv_dtype) {
   return kv_dtype == kKvFp8 && p.q_len == 1 && p.heads >= 1 && p.heads <= kMaxHeads &&
-         p.sparse_idx == nullptr && encode_fn() != nullptr;
+         p.sparse_idx == nullptr && tensor_map_encoder() != nullptr;
 }
 
 cudaError_t launch_partial_f8(const PartialParams& p, cudaStream_t st) {
@@ -1160,7 +1160,10 @@ cudaError_t launch_partial_f8(const PartialParams& p, cudaStream_t st) {
       g_attr_done[listed][dev] = true;
     }
   }
-  if (!p.q_image_ready) f8_q_image_kernel<<<dim3(p.batch, 2), 256, 0, st>>>(p, p.q_image);
+  if (!p.q_image_ready) {
+    e = launch_q_image(p, st);
+    if (e != cudaSuccess) return e;
+  }
   kernel<<<p.num_ctas, kThreads, smem, st>>>(fp);
   return cudaGetLastError();
 }
