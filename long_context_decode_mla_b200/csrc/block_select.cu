@@ -17,20 +17,27 @@
 // index.
 #include "dcpmla.h"
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "q_image.cuh"
 #include "select_topk.cuh"
+#include "tc_ptx.cuh"
 
 namespace dcpmla {
 namespace {
 
 constexpr int kGroups = 5;
-constexpr int kQCodes = 64 * kHeadDim;              // q codes of a row, 64 heads
-constexpr int kQBytes = kQCodes + 64 * kGroups * 4; // then the steps [group][head]
-constexpr int kTile = 128;                          // blocks per scoring tile
+constexpr int kTile = 64;                           // blocks per scoring tile
+constexpr uint32_t kChunk = 8192;                   // 64 rows x 128 bytes
+// Query image of a row: the int8 codes of 64 heads (zeros past the call's) in
+// the scoring kernel's shared-memory order, a 128-byte-swizzled chunk per
+// group (the rope's is half used), then the steps [64 heads][8] (5 used).
+constexpr int kQCodes = kGroups * kChunk;
+constexpr int kQBytes = kQCodes + 64 * 8 * 4;
 
 struct SelectParams {
   const __nv_bfloat16* q;      // [rows][heads][576]
@@ -43,8 +50,9 @@ struct SelectParams {
   int topk, sink, recent;
   int tiles;                   // scoring tiles per row (from the table's stride)
   uint8_t* q_codes;            // [rows][kQBytes]
+  int num_ctas;                // of the scoring kernel
   float* scores;               // [rows][tiles][heads][kTile]
-  float* tile_max;             // [rows][tiles][heads]
+  uint32_t* tile_max;          // [rows][tiles][heads], as ordered keys
   int* out_blocks;             // [rows][topk] or nullptr
   int* out_table;              // [rows][topk]
   int* out_lens;               // [rows]
@@ -64,82 +72,368 @@ __device__ __forceinline__ int rows_of(const SelectParams& p, int r, int* blocks
     nb = p.bt_stride;
     n = nb * kBlock;
   }
-  if (bad && p.flags && threadIdx.x == 0) atomicOr(p.flags, kFlagBadLength);
+  if (bad && p.flags) atomicOr(p.flags, kFlagBadLength);
   *blocks = nb;
   return n;
 }
 
-// int8 codes of one query row: a warp per (head, group).
+// Query image of one row: a warp per group of head blockIdx.y.
 __global__ void __launch_bounds__(160) q_codes_kernel(const SelectParams p) {
   const int r = blockIdx.x, h = blockIdx.y, g = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const __nv_bfloat16* q = p.q + ((size_t)r * p.heads + h) * kHeadDim;
-  const int v = g < 4 ? 4 : 2, d = g < 4 ? 128 * g + 4 * lane : kVDim + 2 * lane;
+  const bool live = h < p.heads;
+  const __nv_bfloat16* q = p.q + ((size_t)r * p.heads + (live ? h : 0)) * kHeadDim;
+  const int v = g < 4 ? 4 : 2, d = v * lane;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   float amax = 0.f;
   for (int e = 0; e < v; ++e) {
-    x[e] = __bfloat162float(q[d + e]);
+    x[e] = live ? __bfloat162float(q[128 * g + d + e]) : 0.f;
     if (!(fabsf(x[e]) <= 3.4028234663852886e38f)) x[e] = 0.f;
     amax = fmaxf(amax, fabsf(x[e]));
   }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float step = amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
+  uint32_t code = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int c = min(127, max(-127, __float2int_rn(__fdiv_rn(x[e], step))));
+    code |= ((uint32_t)c & 0xFFu) << (8 * e);
+  }
   uint8_t* out = p.q_codes + (size_t)r * kQBytes;
-  for (int e = 0; e < v; ++e)
-    out[h * kHeadDim + d + e] = (uint8_t)min(127, max(-127, __float2int_rn(__fdiv_rn(x[e], step))));
-  if (lane == 0) reinterpret_cast<float*>(out + kQCodes)[g * 64 + h] = step;
+  uint8_t* at = out + g * kChunk + qimg::sw128(h, d >> 4) + (d & 15);
+  if (g < 4)
+    *reinterpret_cast<uint32_t*>(at) = code;
+  else
+    *reinterpret_cast<uint16_t*>(at) = (uint16_t)code;
+  if (lane == 0) reinterpret_cast<float*>(out + kQCodes)[h * 8 + g] = step;
 }
 
-// Scores of one tile of blocks of one row: a thread per block.
-__global__ void __launch_bounds__(kTile) score_kernel(const SelectParams p) {
-  const int r = blockIdx.y, tile = blockIdx.x;
-  int nb;
-  rows_of(p, r, &nb);
-  if (tile * kTile >= nb) return;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float wmax[kTile / 32][64];
-  const uint8_t* qc = p.q_codes + (size_t)r * kQBytes;
-  for (int i = threadIdx.x; i < kQBytes / 16; i += kTile)
-    reinterpret_cast<uint4*>(smem)[i] = reinterpret_cast<const uint4*>(qc)[i];
-  __syncthreads();
-  const float* steps = reinterpret_cast<const float*>(smem + kQCodes);
-  const int k = tile * kTile + threadIdx.x;
-  const int b = r / p.q_len;
-  int blk = -1;
-  if (k < nb) {
-    blk = __ldg(p.block_table + (size_t)b * p.bt_stride + k);
-    if (blk < 0 || (long long)blk >= p.num_blocks) {
-      if (p.flags) atomicOr(p.flags, kFlagBadBlock);
-      blk = -1;
+// ----------------------------------------------------------- scoring ----
+//
+// Scores of tiles of 64 blocks on the tensor cores (tcgen05, kind::i8): the
+// summaries' codes are A (M = 64 blocks), the query's B (N = 64 heads), each
+// scale group an int32 accumulator of its own, so that a TMEM lane holds one
+// block for 32 heads.  Summaries are scattered over the pool: four warps copy
+// them in 16-byte pieces (three tiles in flight) into swizzled chunks; warps
+// 0-3 and 4-7 turn alternate tiles into scores, written [head][block], and
+// the heads' maxima over the tile.  The tiles of all rows, end to end, are
+// dealt to the CTAs in contiguous ranges, so that a CTA rarely changes query.
+constexpr int kScoreThreads = 416;
+constexpr int kCopyBase = 256, kCopyThreads = 128, kMmaWarp = 12;
+constexpr int kScoreStages = 3, kBufs = 3;
+constexpr uint32_t kScaleBytes = 64 * 32;
+constexpr uint32_t kStageBytes = kGroups * kChunk + kScaleBytes;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kRowChunk = 512;           // rows looked at together
+
+struct ScoreCtl {
+  uint64_t full[kScoreStages], empty[kScoreStages];
+  uint64_t d_full[kBufs], d_empty[kBufs];
+  uint64_t q_full, q_empty;
+  uint32_t wmax[2][4][32];               // [group][warp of it][head of its half]
+  uint32_t tmem_base;
+  int abort;
+  int warp_sums[16];
+  int end[kRowChunk];                    // tiles up to and including each row of the chunk
+  int blocks[kRowChunk];
+};
+constexpr uint32_t kOffStage = kQCodes + 2048;     // after the query image
+constexpr uint32_t kOffCtl = kOffStage + kScoreStages * kStageBytes;
+constexpr size_t kScoreSmem = kOffCtl + sizeof(ScoreCtl) + 1024;
+static_assert(kQBytes == kQCodes + 2048 && kOffStage % 1024 == 0 && kStageBytes % 1024 == 0 &&
+                  kScoreSmem <= 232448,
+              "shared memory layout");
+
+__device__ __forceinline__ uint64_t dplus(uint64_t d, uint32_t byte_off) {
+  return d + (uint64_t)(byte_off >> 4);
+}
+
+// Tile u of a chunk of rows: its row and place in the row.
+struct TileWalk {
+  int u, hi, row, tile, nb;
+  __device__ __forceinline__ void locate(const ScoreCtl& c, int row_lo) {
+    int a = row_lo, b = kRowChunk - 1;
+    while (a < b) {
+      const int mid = (a + b) >> 1;
+      if (c.end[mid] > u) b = mid; else a = mid + 1;
     }
+    row = a;
+    tile = u - (a > 0 ? c.end[a - 1] : 0);
+    nb = c.blocks[a];
   }
-  const uint8_t* rec = p.summaries + (size_t)max(blk, 0) * kSummaryBytes;
-  float sc[kGroups];
-  for (int g = 0; g < kGroups; ++g) sc[g] = reinterpret_cast<const float*>(rec + kHeadDim)[g];
-  float* out = p.scores + ((size_t)r * p.tiles + tile) * p.heads * kTile;
-  for (int h = 0; h < p.heads; ++h) {
-    float s = 0.f;
-    for (int g = 0; g < kGroups; ++g) {
-      int dot = 0;
-      const int words = g < 4 ? 32 : 16;
-      for (int w = 0; w < words; ++w)
-        dot = __dp4a(reinterpret_cast<const int*>(smem + h * kHeadDim + 128 * g)[w],
-                     reinterpret_cast<const int*>(rec + 128 * g)[w], dot);
-      const float t = __fmul_rn((float)dot, __fmul_rn(steps[g * 64 + h], sc[g]));
-      s = g == 0 ? t : __fadd_rn(s, t);
+  __device__ __forceinline__ bool start(const ScoreCtl& c, int lo, int hi_) {
+    u = lo;
+    hi = hi_;
+    if (u >= hi) return false;
+    locate(c, 0);
+    return true;
+  }
+  __device__ __forceinline__ bool last_of_row() const {
+    return (tile + 1) * kTile >= nb || u + 1 >= hi;
+  }
+  __device__ __forceinline__ bool next(const ScoreCtl& c) {
+    if (++u >= hi) return false;
+    if ((tile + 1) * kTile < nb) {
+      ++tile;
+      return true;
     }
-    if (blk < 0) s = -INFINITY;
-    out[h * kTile + threadIdx.x] = s;
-    float m = s;
+    locate(c, row + 1);
+    return true;
+  }
+};
+
+// Copies of every tile (four warps) and of each row's query image.
+__device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, uint8_t* base, int r0,
+                                          int lo, int hi, uint32_t& tau, uint32_t& sigma) {
+  const int t = threadIdx.x - kCopyBase;
+  TileWalk w;
+  if (!w.start(c, lo, hi)) return;
+  bool fresh = true;
+  while (true) {
+    const uint32_t s = tau % kScoreStages;
+    if (tau >= (uint32_t)kScoreStages &&
+        !ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort))
+      return;
+    const int r = r0 + w.row;
+    const int* table = p.block_table + (size_t)(r / p.q_len) * p.bt_stride + w.tile * kTile;
+    uint8_t* stage = base + kOffStage + s * kStageBytes;
+    const uint32_t dst = ptx::smem_addr(stage);
+    const int n = min(kTile, w.nb - w.tile * kTile);
+    // sixteen lanes take a row's 38 pieces; rows past the tile's end are left
+    // as they are (they only reach their own lanes)
+    const int un0 = t & 15;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5][h] = m;
+    for (int k = 0; k < 8; ++k) {
+      const int row = (t >> 4) + 8 * k;
+      if (row < n) {
+        int blk = __ldg(table + row);
+        if (blk < 0 || (long long)blk >= p.num_blocks) {
+          if (un0 == 0 && p.flags) atomicOr(p.flags, kFlagBadBlock);
+          blk = 0;
+        }
+        const uint8_t* src = p.summaries + (size_t)blk * kSummaryBytes;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int un = un0 + 16 * j;
+          if (un < 36)
+            ptx::cp_async16(dst + (un >> 3) * kChunk + qimg::sw128(row, un & 7), src + 16 * un, 16);
+          else if (un < 38)
+            ptx::cp_async16(dst + kGroups * kChunk + row * 32 + (un - 36) * 16, src + 16 * un, 16);
+        }
+      }
+    }
+    ptx::cp_async_arrive(&c.full[s]);
+    if (fresh) {
+      if (t == 0) {
+        if (sigma > 0 && !ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort)) return;
+        // the scorers read the old steps through the generic proxy
+        ptx::fence_proxy_async();
+        ptx::mbar_arrive_expect_tx(&c.q_full, kQBytes);
+        ptx::bulk_g2s(ptx::smem_addr(base), p.q_codes + (size_t)r * kQBytes, kQBytes, &c.q_full);
+      }
+      ++sigma;
+    }
+    fresh = w.last_of_row();
+    ++tau;
+    if (!w.next(c)) break;
   }
+}
+
+__device__ __forceinline__ void score_mma_role(ScoreCtl& c, uint8_t* base, int lo, int hi,
+                                               uint32_t& tau, uint32_t& sigma) {
+  constexpr uint32_t kId = ptx::idesc_i8(64, 64);
+  const uint64_t dq = ptx::sdesc(ptx::smem_addr(base), 16, 1024, ptx::kSwizzle128B);
+  const uint64_t dk0 = ptx::sdesc(ptx::smem_addr(base + kOffStage), 16, 1024, ptx::kSwizzle128B);
+  TileWalk w;
+  if (!w.start(c, lo, hi)) return;
+  bool fresh = true;
+  while (true) {
+    const uint32_t s = tau % kScoreStages, buf = tau % kBufs;
+    if (fresh) {
+      if (!ptx::mbar_wait(&c.q_full, sigma & 1, &c.abort)) return;
+      ++sigma;
+    }
+    if (tau >= (uint32_t)kBufs &&
+        !ptx::mbar_wait(&c.d_empty[buf], ((tau / kBufs) + 1) & 1, &c.abort))
+      return;
+    if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
+    ptx::tc_fence_after();
+    ptx::fence_proxy_async();      // the copies were made through the generic proxy
+    const uint64_t dk = dplus(dk0, s * kStageBytes);
+    const uint32_t d = c.tmem_base + buf * (32 * kGroups);
+#pragma unroll 1
+    for (int g = 0; g < kGroups; ++g)
+      for (int ks = 0; ks < (g < 4 ? 4 : 2); ++ks)
+        ptx::mma_ws_i8(d + 32 * g, dplus(dk, g * kChunk + ks * 32), dplus(dq, g * kChunk + ks * 32),
+                       kId, ks > 0);
+    ptx::mma_commit(&c.empty[s]);
+    ptx::mma_commit(&c.d_full[buf]);
+    fresh = w.last_of_row();
+    if (fresh) ptx::mma_commit(&c.q_empty);
+    ++tau;
+    if (!w.next(c)) break;
+  }
+}
+
+__device__ __forceinline__ void score_role(const SelectParams& p, ScoreCtl& c, uint8_t* base, int r0,
+                                           int lo, int hi, uint32_t& tau, uint32_t& sigma) {
+  const int group = threadIdx.x >> 7, t = threadIdx.x & 127;
+  const int row = t & 63, hh = t >> 6, lane = t & 31, warp = t >> 5;
+  const uint32_t lane_base = c.tmem_base + ((uint32_t)(warp * 32) << 16);
+  const float* steps = reinterpret_cast<const float*>(base + kQCodes);
+  TileWalk w;
+  if (!w.start(c, lo, hi)) return;
+  bool fresh = true;
+  while (true) {
+    if (fresh) {
+      // both groups follow every row, so that each knows which image is in place
+      if (!ptx::mbar_wait(&c.q_full, sigma & 1, &c.abort)) return;
+      ++sigma;
+    }
+    fresh = w.last_of_row();
+    if ((int)(tau & 1) == group) {
+      const uint32_t s = tau % kScoreStages, buf = tau % kBufs;
+      if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
+      const uint8_t* sp = base + kOffStage + s * kStageBytes + kGroups * kChunk + row * 32;
+      const float4 s4 = *reinterpret_cast<const float4*>(sp);
+      const float sc[kGroups] = {s4.x, s4.y, s4.z, s4.w, *reinterpret_cast<const float*>(sp + 16)};
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.empty[s]);
+      const int r = r0 + w.row, k = w.tile * kTile + row;
+      bool live = k < w.nb;
+      if (live) {
+        const int blk = __ldg(p.block_table + (size_t)(r / p.q_len) * p.bt_stride + k);
+        live = blk >= 0 && (long long)blk < p.num_blocks;
+      }
+      if (!ptx::mbar_wait(&c.d_full[buf], (tau / kBufs) & 1, &c.abort)) return;
+      __syncwarp();
+      ptx::tc_fence_after();
+      float* out = p.scores + ((size_t)r * p.tiles + w.tile) * p.heads * kTile + row;
+#pragma unroll
+      for (int piece = 0; piece < 2; ++piece) {
+        const int h0 = 32 * hh + 16 * piece;
+        uint32_t x[kGroups][16];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          ptx::tmem_ld16(lane_base + buf * (32 * kGroups) + 32 * g + 16 * piece, x[g]);
+        ptx::tmem_wait_ld();
+        if (piece == 1) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&c.d_empty[buf]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (h0 + e < p.heads) {
+            const float4 q4 = *reinterpret_cast<const float4*>(steps + (h0 + e) * 8);
+            const float q5 = steps[(h0 + e) * 8 + 4];
+            const float qs[kGroups] = {q4.x, q4.y, q4.z, q4.w, q5};
+            float v = 0.f;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              const float term = __fmul_rn((float)(int)x[g][e], __fmul_rn(qs[g], sc[g]));
+              v = g == 0 ? term : __fadd_rn(v, term);
+            }
+            if (!live) v = -INFINITY;
+            out[(size_t)(h0 + e) * kTile] = v;
+            const uint32_t m = __reduce_max_sync(0xffffffffu, topk::key_of(v));
+            if (lane == 0) c.wmax[group][warp][16 * piece + e] = m;
+          }
+        }
+      }
+      ptx::named_bar(1 + group, 128);
+      if (t < p.heads)
+        p.tile_max[((size_t)r * p.tiles + w.tile) * p.heads + t] =
+            max(c.wmax[group][2 * (t >> 5)][t & 31], c.wmax[group][2 * (t >> 5) + 1][t & 31]);
+      ptx::named_bar(1 + group, 128);
+    }
+    // the row's steps are read (both groups arrive, once a row)
+    if (fresh) {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.q_empty);
+    }
+    ++tau;
+    if (!w.next(c)) break;
+  }
+}
+
+__global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  ScoreCtl& c = *reinterpret_cast<ScoreCtl*>(base + kOffCtl);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kScoreStages; ++s) {
+      ptx::mbar_init(&c.full[s], kCopyThreads);
+      ptx::mbar_init(&c.empty[s], 5);        // the MMAs' commit, four warps' scale reads
+    }
+    for (int k = 0; k < kBufs; ++k) {
+      ptx::mbar_init(&c.d_full[k], 1);
+      ptx::mbar_init(&c.d_empty[k], 4);
+    }
+    ptx::mbar_init(&c.q_full, 1);
+    ptx::mbar_init(&c.q_empty, 1 + 8);       // the MMAs' commit, eight warps' step reads
+    c.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0) ptx::tmem_alloc(&c.tmem_base, kTmemCols);
+  ptx::fence_proxy_async();
+  ptx::tc_fence_before();
   __syncthreads();
-  if (threadIdx.x < p.heads)
-    p.tile_max[((size_t)r * p.tiles + tile) * p.heads + threadIdx.x] =
-        fmaxf(fmaxf(wmax[0][threadIdx.x], wmax[1][threadIdx.x]),
-              fmaxf(wmax[2][threadIdx.x], wmax[3][threadIdx.x]));
+  ptx::tc_fence_after();
+  const int rows = p.batch * p.q_len;
+  uint32_t tau = 0, sigma = 0;
+  for (int r0 = 0; r0 < rows; r0 += kRowChunk) {
+    int total = 0;
+    for (int i0 = 0; i0 < kRowChunk; i0 += kScoreThreads) {
+      const int i = i0 + threadIdx.x;
+      int nb = 0;
+      if (i < kRowChunk && r0 + i < rows) rows_of(p, r0 + i, &nb);
+      const int nt = (nb + kTile - 1) / kTile;
+      int tot;
+      const int ex = block_exclusive_scan(nt, c.warp_sums, &tot);
+      if (i < kRowChunk) {
+        c.end[i] = total + ex + nt;
+        c.blocks[i] = nb;
+      }
+      total += tot;
+    }
+    __syncthreads();
+    const int lo = (int)((long long)blockIdx.x * total / gridDim.x);
+    const int hi = (int)((long long)(blockIdx.x + 1) * total / gridDim.x);
+    if (warp < 8) {
+      score_role(p, c, base, r0, lo, hi, tau, sigma);
+    } else if (warp < kMmaWarp) {
+      copy_role(p, c, base, r0, lo, hi, tau, sigma);
+    } else {
+      if ((threadIdx.x & 31) == 0) score_mma_role(c, base, lo, hi, tau, sigma);
+    }
+    __syncthreads();
+    if (c.abort) break;
+  }
+  // Drain: every asynchronous arrival and copy lands before the CTA exits.
+  if (threadIdx.x == kMmaWarp * 32) {
+    for (uint32_t s = 0; s < (uint32_t)kScoreStages; ++s) {
+      const uint32_t u = tau > s ? (tau - s + kScoreStages - 1) / kScoreStages : 0;
+      if (u > 0) ptx::mbar_wait(&c.empty[s], (u - 1) & 1, &c.abort);
+    }
+    for (uint32_t k = 0; k < (uint32_t)kBufs; ++k) {
+      const uint32_t u = tau > k ? (tau - k + kBufs - 1) / kBufs : 0;
+      if (u > 0) ptx::mbar_wait(&c.d_full[k], (u - 1) & 1, &c.abort);
+    }
+    if (sigma > 0) ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort);
+  }
+  if (warp >= 8 && warp < kMmaWarp) {
+    ptx::cp_async_wait_all();
+    if (threadIdx.x == kCopyBase && sigma > 0)
+      ptx::mbar_wait(&c.q_full, (sigma - 1) & 1, &c.abort);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (c.abort && threadIdx.x == 0 && p.flags) atomicOr(p.flags, DCPMLA_FLAG_TIMEOUT);
+  if (warp == 0) ptx::tmem_dealloc(c.tmem_base, kTmemCols);
 }
 
 // Ranks and the choice of one row: one cluster.
@@ -159,10 +453,10 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   const int want = min(nb, p.topk);
   const int tiles = (nb + kTile - 1) / kTile;
   if (threadIdx.x < p.heads) {
-    float m = -INFINITY;
+    uint32_t m = 0;
     for (int t = 0; t < tiles; ++t)
-      m = fmaxf(m, p.tile_max[((size_t)r * p.tiles + t) * p.heads + threadIdx.x]);
-    hmax[threadIdx.x] = m;
+      m = max(m, p.tile_max[((size_t)r * p.tiles + t) * p.heads + threadIdx.x]);
+    hmax[threadIdx.x] = topk::value_of(m);
   }
   __syncthreads();
   for (int k = lo + threadIdx.x; k < hi; k += topk::kThreads) {
@@ -250,6 +544,9 @@ cudaError_t prepare_device(int dev) {
   cudaError_t e = cudaFuncSetAttribute(choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        208 * 1024);
   if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kScoreSmem);
+  if (e != cudaSuccess) return e;
   g_done[dev] = true;
   return cudaSuccess;
 }
@@ -298,8 +595,8 @@ int check_select(const SelectArgs& a, SelectParams* p) {
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   const int rows = p.batch * p.q_len;
-  q_codes_kernel<<<dim3(rows, p.heads), 160, 0, st>>>(p);
-  score_kernel<<<dim3(p.tiles, rows), kTile, kQBytes, st>>>(p);
+  q_codes_kernel<<<dim3(rows, 64), 160, 0, st>>>(p);
+  score_kernel<<<p.num_ctas, kScoreThreads, kScoreSmem, st>>>(p);
   const int size = p.bt_stride <= 4096 ? 1 : kMaxCluster;
   const int words = topk::slice_words(p.bt_stride, size);
   return topk::launch(choose_kernel, rows, size, (size_t)words * 33 * 4, st, p, words);
@@ -311,10 +608,13 @@ int run_select(SelectParams& p, uint8_t* ws, cudaStream_t st) {
   if (cudaGetDevice(&dev) != cudaSuccess) return DCPMLA_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevicesConfigured) return DCPMLA_ERR_UNSUPPORTED;
   if (prepare_device(dev) != cudaSuccess) return DCPMLA_ERR_CUDA;
+  int rc = dcpmla_device_sm_count(&p.num_ctas);
+  if (rc != DCPMLA_OK) return rc;
+  p.num_ctas = (int)std::min<long long>(p.num_ctas, (long long)p.batch * p.q_len * p.tiles);
   const SelectLayout l = layout(p.batch * p.q_len, p.heads, p.bt_stride);
   p.q_codes = ws + l.q_codes;
   p.scores = reinterpret_cast<float*>(ws + l.scores);
-  p.tile_max = reinterpret_cast<float*>(ws + l.tile_max);
+  p.tile_max = reinterpret_cast<uint32_t*>(ws + l.tile_max);
   return launch_select(p, st) == cudaSuccess ? DCPMLA_OK : DCPMLA_ERR_CUDA;
 }
 

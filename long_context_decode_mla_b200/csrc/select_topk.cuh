@@ -39,6 +39,11 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The value of a key that is not NaN's.
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
 // Sum of `share[which]` over the CTAs before this one (call between cluster
 // barriers that order the writes and the next reuse).
 __device__ __forceinline__ int before(cg::cluster_group& cl, Ctl& c, int which) {

@@ -266,6 +266,16 @@ __device__ __forceinline__ void mma_ws_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// Weight-stationary int8 form (kind::i8, int32 accumulation: exact).
+__device__ __forceinline__ void mma_ws_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.ws.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Weight-stationary MMAs that keep the B operand in one of the tensor
 // core's four collector buffers: kFill reads B from shared memory and keeps
 // it, kUse / kLastUse read the kept copy (kLastUse releases it) instead of
@@ -402,6 +412,12 @@ __host__ __device__ constexpr uint32_t idesc_make(int M, int N, uint32_t fmt, bo
                                                   bool b_mn) {
   return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Instruction descriptor, kind::i8 with signed inputs and int32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
 
 // Instruction descriptor, kind::f16 with fp16 inputs and fp32 accumulation.
