@@ -9,24 +9,28 @@
 //
 // With the LSE given there is no softmax to carry from row to row: a row's
 // weight needs its own scores only.  So the scores are computed transposed to
-// the decode kernels', D = K Q^T with the 64 rows of a cache block as M and the
-// (query, head) rows as N: a TMEM lane then holds one cached row for 32 heads,
-// a row's fp32 scales are one thread's registers, and the sum over heads stays
-// in a thread but for one exchange between the two lane halves.  Rows past a
+// the decode kernels', D = K Q^T with the cached rows as M and the (query, head)
+// rows as N: a TMEM lane then holds one cached row for all heads, a row's fp32
+// scales are one thread's registers, and the sum over heads stays in a thread
+// but for one exchange between two.  Rows past a
 // request's end only ever reach their own lanes, so nothing is cleared.
 //
 //  * fp8 rows: the e4m3 codes are the A operand as they are; Q comes as the
 //    decode kernel's operand image (two e4m3 terms in one power-of-two frame,
-//    q_image.cuh).  Every 128-value scale group has an accumulator of its own,
-//    scaled in fp32, and the bf16 rope a fifth.
-//  * bf16 rows and queries multiply as they are (exact products).
+//    q_image.cuh).  Every 128-value scale group is a part with an accumulator of
+//    its own, scaled in fp32, and the bf16 rope a fifth.
+//  * bf16 rows and queries multiply as they are (exact products), in one part.
 //
-// A tile is one cache block, loaded by TMA into a stage of its own (fp8: three
-// stages of 41 KB; bf16: two of 72 KB), prefetched into L2 six tiles ahead.
-// Warps 0-3 and 4-7 turn alternate tiles into weights; warp 8 loads; warp 9
-// issues the MMAs (36 a tile).  Tiles are dealt to the CTAs as in decode.  Each
-// row is summed by the same threads in the same order whatever the number of
-// CTAs: no atomics, the same bits every time.  Every wait is bounded.
+// A tile is two cache blocks (M = 128: a weight-stationary M = 64 MMA takes as
+// long, and 36 of them more than a block's share of HBM time).  Its rows go
+// through a ring of eight 16 KB slots, 128 bytes of every row each, loaded by
+// TMA and given back slot by slot, with whole blocks prefetched into L2 ahead.
+// Warp 8 loads; warps 9 and 10 issue the MMAs (36 a tile); warps 0-3 and 4-7 add each
+// part into the scores of 32 heads a thread, so that a part's accumulator is
+// free again as soon as it is read, and exchange the sums of their halves.
+// Tiles are dealt to the CTAs as in decode.  Each row is summed by the same
+// threads in the same order whatever the number of CTAs: no atomics, the same
+// bits every time.  Every wait is bounded.
 #include "dcpmla.h"
 
 #include <cuda.h>
@@ -54,38 +58,49 @@ struct MassParams {
   CUtensorMap q;         // bf16: [batch][rows][1152] u8, box 128 x 64, rows past the pass zero
 };
 
-constexpr int kThreads = 320;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kGroupThreads = 128;
-constexpr uint32_t kChunk = 8192;                  // 64 rows x 128 bytes
-constexpr int kBufs = 3;                           // TMEM accumulator sets
-constexpr uint32_t kTmemCols = 512;
-constexpr int kPrefetchTiles = 6;
+constexpr int kThreads = 352;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;         // fp8: and warp 10
+constexpr int kWeightThreads = 256;
+constexpr uint32_t kHalf = 8192;                   // 64 rows x 128 bytes
+constexpr uint32_t kSlot = 2 * kHalf;              // of a tile's two blocks
+constexpr int kSlots = 8;
+constexpr int kBufs = 8;                           // TMEM accumulators of 64 columns
+constexpr uint32_t kTmemCols = 64 * kBufs;
+constexpr uint32_t kQBytes = 9 * kHalf;            // fp8: hi, lo, rope; bf16: nine chunks
+#ifndef KPF
+#define KPF 1
+#endif
+constexpr int kPrefetchTiles = KPF;
 constexpr int kMaxSeg = 64;
+constexpr int kTileMass = 128;                     // rows of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int kDtype>
 struct Shape;
+// kMeta tiles can be between their load and their weights at once: eight slots
+// and eight accumulators hold 3.2 fp8 tiles of five parts, or 0.9 and 8 bf16
+// tiles (accumulated in one part).
 template <>
 struct Shape<kKvFp8> {
-  static constexpr int kRowBytes = kRowBytesFp8, kStages = 3, kChunks = 5, kParts = 5;
-  static constexpr uint32_t kStageBytes = 5 * kChunk + 1024, kScales = 5 * kChunk;
-  static constexpr uint32_t kQBytes = 9 * kChunk;   // hi, lo, rope
+  static constexpr int kRowBytes = kRowBytesFp8, kChunks = 5, kParts = 5, kMeta = 4,
+                       kIssuers = 2;
 };
 template <>
 struct Shape<kKvBf16> {
-  static constexpr int kRowBytes = kRowBytesBf16, kStages = 2, kChunks = 9, kParts = 1;
-  static constexpr uint32_t kStageBytes = 9 * kChunk, kScales = 0;
-  static constexpr uint32_t kQBytes = 9 * kChunk;
+  static constexpr int kRowBytes = kRowBytesBf16, kChunks = 9, kParts = 1, kMeta = 10,
+                       kIssuers = 1;
 };
+constexpr int kMaxMeta = 10;
+constexpr uint32_t kScaleBytes = kTileMass * 16;   // fp8: four fp32 scales a row
 
 struct Ctl {
-  uint64_t full[3], empty[3];          // per stage: bytes landed / MMAs and reads done
-  uint64_t d_full[kBufs], d_empty[kBufs];
+  uint64_t full[kSlots], empty[kSlots];      // a slot's bytes landed / its MMAs done
+  uint64_t d_full[kBufs], d_empty[kBufs];    // an accumulator done / read
+  uint64_t meta[kMaxMeta];                   // a tile's row counts written and scales landed
   uint64_t q_full, q_empty;
-  alignas(16) float2 head[2][64];      // per weight group: 2^-a scale log2(e), lse log2(e)
-  float half[2][2][64];                // [group][parity]: the other lane half's sums
-  int nv[3];                           // rows of the stage's tile that take part
+  alignas(16) float2 head[64];               // 2^-a scale log2(e), lse log2(e)
+  float half[2][kTileMass];                  // [tile parity]: the other half's sums
+  int nv[kMaxMeta][2];                       // rows of each block that take part
   uint32_t tmem_base;
   int abort;
   int sel_count;
@@ -94,11 +109,15 @@ struct Ctl {
 };
 
 template <int kDtype>
+constexpr uint32_t ctl_offset() {
+  return kQBytes + kSlots * kSlot + (kDtype == kKvFp8 ? Shape<kDtype>::kMeta * kScaleBytes : 0);
+}
+template <int kDtype>
 constexpr size_t smem_bytes() {
-  return Shape<kDtype>::kQBytes + (size_t)Shape<kDtype>::kStages * Shape<kDtype>::kStageBytes +
-         sizeof(Ctl) + 1024;
+  return ctl_offset<kDtype>() + sizeof(Ctl) + 1024;
 }
 static_assert(smem_bytes<kKvFp8>() <= 232448 && smem_bytes<kKvBf16>() <= 232448, "shared memory");
+constexpr uint32_t kOffSlot = kQBytes, kOffScale = kQBytes + kSlots * kSlot;
 
 __device__ __forceinline__ uint64_t dplus(uint64_t d, uint32_t byte_off) {
   return d + (uint64_t)(byte_off >> 4);
@@ -109,57 +128,113 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-struct Counts {
-  uint32_t tau = 0, sigma = 0;     // tiles and requests handled so far
+// Walks the CTA's tiles: two blocks of one segment each.
+struct PairCursor {
+  int k, t, nseg, nt;
+  SegView v;
+  __device__ __forceinline__ bool open(const PartialParams& p, const Ctl& c) {
+    for (; k < nseg; ++k) {
+      v = seg_view(p, c, k);
+      nt = (v.nrows + kTileMass - 1) / kTileMass;
+      if (nt > 0) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool start(const PartialParams& p, const Ctl& c, int n) {
+    nseg = n;
+    k = t = 0;
+    return open(p, c);
+  }
+  __device__ __forceinline__ bool next(const PartialParams& p, const Ctl& c) {
+    if (++t < nt) return true;
+    t = 0;
+    ++k;
+    return open(p, c);
+  }
+  __device__ __forceinline__ bool last_of_segment() const { return t == nt - 1; }
+  // rows of block half `i` of the tile that lie in the segment (0: no block)
+  __device__ __forceinline__ int rows(int i) const {
+    return max(0, min(kBlock, v.nrows - t * kTileMass - i * kBlock));
+  }
+  __device__ __forceinline__ int block(int i) const { return (v.row_begin >> 6) + 2 * t + i; }
 };
 
-// TMA loads of every tile, and of each request's Q once the previous
-// request's MMAs are done with it.
+// Counters of one thread's way through the tiles, kept across segment batches.
+struct Counts {
+  uint32_t tau = 0, chunk = 0, part = 0, sigma = 0;
+};
+
+// TMA loads of every tile, slot by slot, and of each request's Q once the
+// previous request's MMAs are done with it.
 template <int kDtype>
 __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* base, int nseg,
                                           Counts& n) {
   using S = Shape<kDtype>;
   const PartialParams& p = m.p;
-  TileCursor cur, pf;
+  PairCursor cur, pf;
   if (!cur.start(p, c, nseg)) return;
   pf = cur;
   bool pf_ok = true;
-  constexpr uint32_t kTile = 64 * S::kRowBytes;
+  constexpr uint32_t kBlockBytes = 64 * S::kRowBytes;
   auto prefetch = [&]() {
     if (!pf_ok) return;
-    const int blk = tile_block(p, pf.v.b, (pf.v.row_begin >> 6) + pf.t);
-    if (blk >= 0) ptx::prefetch_l2(p.kv + (size_t)blk * kTile, kTile);
+    for (int i = 0; i < 2; ++i)
+      if (pf.rows(i) > 0) {
+        const int blk = tile_block(p, pf.v.b, pf.block(i));
+        if (blk >= 0) ptx::prefetch_l2(p.kv + (size_t)blk * kBlockBytes, kBlockBytes);
+      }
     pf_ok = pf.next(p, c);
   };
   for (int i = 0; i < kPrefetchTiles; ++i) prefetch();
   while (true) {
-    const uint32_t s = n.tau % S::kStages;
-    if (n.tau >= (uint32_t)S::kStages &&
-        !ptx::mbar_wait(&c.empty[s], ((n.tau / S::kStages) + 1) & 1, &c.abort))
-      return;
-    const int blk = tile_block(p, cur.v.b, (cur.v.row_begin >> 6) + cur.t);
-    const int z = blk >= 0 ? blk : 0;        // a bad entry: a stand-in block, no rows
-    c.nv[s] = blk >= 0 ? cur.tile_valid_rows() : 0;
-    const uint32_t dst = ptx::smem_addr(base + S::kQBytes + s * S::kStageBytes);
-    ptx::mbar_arrive_expect_tx(&c.full[s], kTile);
+    // a bad table entry: a stand-in block, no rows; a missing second block: nothing
+    int blk[2], halves = 1;
+    const uint32_t meta = n.tau % S::kMeta;
 #pragma unroll
-    for (int k = 0; k < S::kChunks; ++k)
-      ptx::tma_load_3d(dst + k * kChunk, &m.rows, kDtype == kKvFp8 && k == 4 ? 528 : 128 * k, 0, z,
-                       &c.full[s]);
-    if constexpr (kDtype == kKvFp8)
-      ptx::tma_load_3d(dst + S::kScales, &m.scales, 512, 0, z, &c.full[s]);
-    if (cur.t == 0) {
-      if (n.sigma > 0 && !ptx::mbar_wait(&c.q_empty, (n.sigma - 1) & 1, &c.abort)) return;
-      const uint32_t dq = ptx::smem_addr(base);
-      ptx::mbar_arrive_expect_tx(&c.q_full, S::kQBytes);
-      if constexpr (kDtype == kKvFp8) {
-        ptx::bulk_g2s(dq, p.q_image + (size_t)cur.v.b * kQImageBytes, S::kQBytes, &c.q_full);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 9; ++k)
-          ptx::tma_load_3d(dq + k * kChunk, &m.q, 128 * k, 0, cur.v.b, &c.q_full);
+    for (int i = 0; i < 2; ++i) {
+      const int rows = cur.rows(i);
+      blk[i] = rows > 0 ? tile_block(p, cur.v.b, cur.block(i)) : -1;
+      if (i == 1 && rows > 0) halves = 2;
+    }
+#pragma unroll 1
+    for (int k = 0; k < S::kChunks; ++k) {
+      const uint32_t s = n.chunk % kSlots;
+      if (n.chunk >= (uint32_t)kSlots &&
+          !ptx::mbar_wait(&c.empty[s], ((n.chunk / kSlots) + 1) & 1, &c.abort))
+        return;
+      if (k == 0) {
+        // the tile kMeta before this one has been turned into weights by now
+        // (Shape): its row counts and scales can go
+        c.nv[meta][0] = blk[0] >= 0 ? cur.rows(0) : 0;
+        c.nv[meta][1] = blk[1] >= 0 ? cur.rows(1) : 0;
+        if constexpr (kDtype == kKvFp8) {
+          ptx::mbar_arrive_expect_tx(&c.meta[meta], halves * 1024);
+          for (int i = 0; i < halves; ++i)
+            ptx::tma_load_3d(ptx::smem_addr(base + kOffScale + meta * kScaleBytes + i * 1024),
+                             &m.scales, 512, 0, max(blk[i], 0), &c.meta[meta]);
+        } else {
+          ptx::mbar_arrive(&c.meta[meta]);
+        }
       }
-      ++n.sigma;
+      const uint32_t dst = ptx::smem_addr(base + kOffSlot + s * kSlot);
+      ptx::mbar_arrive_expect_tx(&c.full[s], halves * kHalf);
+      for (int i = 0; i < halves; ++i)
+        ptx::tma_load_3d(dst + i * kHalf, &m.rows, kDtype == kKvFp8 && k == 4 ? 528 : 128 * k, 0,
+                         max(blk[i], 0), &c.full[s]);
+      ++n.chunk;
+      if (k == 0 && cur.t == 0) {
+        if (n.sigma > 0 && !ptx::mbar_wait(&c.q_empty, (n.sigma - 1) & 1, &c.abort)) return;
+        const uint32_t dq = ptx::smem_addr(base);
+        ptx::mbar_arrive_expect_tx(&c.q_full, kQBytes);
+        if constexpr (kDtype == kKvFp8) {
+          ptx::bulk_g2s(dq, p.q_image + (size_t)cur.v.b * kQImageBytes, kQBytes, &c.q_full);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < 9; ++j)
+            ptx::tma_load_3d(dq + j * kHalf, &m.q, 128 * j, 0, cur.v.b, &c.q_full);
+        }
+        ++n.sigma;
+      }
     }
     ++n.tau;
     prefetch();
@@ -167,166 +242,191 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
   }
 }
 
-// D = K Q^T of every tile (weight-stationary M = 64 rows, N = 64 heads, 32
-// TMEM columns a part).
+// D = K Q^T (M = 128 rows, N = 64 heads, 64 TMEM columns a part).  A wait
+// costs an issuing thread some 600 cycles while the tensor core streams its
+// operands, as much as eight MMAs take: fp8 parts alternate between two issuers
+// (77 cycles an MMA, 36 a tile), and bf16, whose chunks accumulate in one part
+// and so keep to one thread, waits for three chunks at a time.
 template <int kDtype>
 __device__ __forceinline__ void mma_role(const MassParams& m, Ctl& c, uint8_t* base, int nseg,
-                                         Counts& n) {
+                                         uint32_t side, Counts& n) {
   using S = Shape<kDtype>;
-  constexpr uint32_t kIdF8 = ptx::idesc_make(64, 64, 0, false, false);
-  constexpr uint32_t kIdBf = ptx::idesc_make(64, 64, 1, false, false);
+  constexpr uint32_t kIdF8 = ptx::idesc_make(128, 64, 0, false, false);
+  constexpr uint32_t kIdBf = ptx::idesc_make(128, 64, 1, false, false);
   const uint64_t dq = ptx::sdesc(ptx::smem_addr(base), 16, 1024, ptx::kSwizzle128B);
-  const uint64_t dk0 = ptx::sdesc(ptx::smem_addr(base + S::kQBytes), 16, 1024, ptx::kSwizzle128B);
-  TileCursor cur;
+  const uint64_t dk0 = ptx::sdesc(ptx::smem_addr(base + kOffSlot), 16, 1024, ptx::kSwizzle128B);
+  PairCursor cur;
   if (!cur.start(m.p, c, nseg)) return;
   while (true) {
-    const uint32_t s = n.tau % S::kStages, buf = n.tau % kBufs;
     if (cur.t == 0) {
       if (!ptx::mbar_wait(&c.q_full, n.sigma & 1, &c.abort)) return;
       ++n.sigma;
     }
-    if (n.tau >= (uint32_t)kBufs &&
-        !ptx::mbar_wait(&c.d_empty[buf], ((n.tau / kBufs) + 1) & 1, &c.abort))
-      return;
-    if (!ptx::mbar_wait(&c.full[s], (n.tau / S::kStages) & 1, &c.abort)) return;
-    ptx::tc_fence_after();
-    const uint64_t dk = dplus(dk0, s * S::kStageBytes);
-    const uint32_t d = c.tmem_base + buf * (32 * S::kParts);
     if constexpr (kDtype == kKvFp8) {
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g)
+      for (int k = 0; k < S::kChunks; ++k, ++n.chunk, ++n.part) {
+        if ((n.chunk & 1) != side) continue;
+        const uint32_t s = n.chunk % kSlots, buf = n.part % kBufs;
+        uint64_t* reuse = n.part >= (uint32_t)kBufs ? &c.d_empty[buf] : &c.full[s];
+        const uint32_t parity = (n.chunk / kSlots) & 1;
+        if (!ptx::mbar_wait3(&c.full[s], parity, reuse,
+                             n.part >= (uint32_t)kBufs ? ((n.part / kBufs) + 1) & 1 : parity,
+                             &c.full[s], parity, &c.abort))
+          return;
+        ptx::tc_fence_after();
+        const uint64_t dk = dplus(dk0, s * kSlot);
+        const uint32_t d = c.tmem_base + 64 * buf;
+        if (k < 4) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const uint32_t off = g * kChunk + ks * 32;
-          ptx::mma_ws_f8(d + 32 * g, dplus(dk, off), dplus(dq, off), kIdF8, ks > 0);
-          ptx::mma_ws_f8(d + 32 * g, dplus(dk, off), dplus(dq, 4 * kChunk + off), kIdF8, 1u);
+          for (int ks = 0; ks < 4; ++ks) {
+            ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, k * kHalf + ks * 32), kIdF8, ks > 0);
+            ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, (4 + k) * kHalf + ks * 32), kIdF8, 1u);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            ptx::mma_f16(d, dplus(dk, ks * 32), dplus(dq, 8 * kHalf + ks * 32), kIdBf, ks > 0);
         }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        ptx::mma_ws_f16(d + 128, dplus(dk, 4 * kChunk + ks * 32), dplus(dq, 8 * kChunk + ks * 32),
-                        kIdBf, ks > 0);
+        ptx::mma_commit(&c.empty[s]);
+        ptx::mma_commit(&c.d_full[buf]);
+      }
     } else {
+      const uint32_t buf = n.part % kBufs;
+      if (n.part >= (uint32_t)kBufs &&
+          !ptx::mbar_wait(&c.d_empty[buf], ((n.part / kBufs) + 1) & 1, &c.abort))
+        return;
+      const uint32_t d = c.tmem_base + 64 * buf;
 #pragma unroll 1
-      for (int k = 0; k < 9; ++k)
+      for (int k3 = 0; k3 < S::kChunks; k3 += 3) {
+        const uint32_t c0 = n.chunk, c1 = c0 + 1, c2 = c0 + 2;
+        if (!ptx::mbar_wait3(&c.full[c0 % kSlots], (c0 / kSlots) & 1, &c.full[c1 % kSlots],
+                             (c1 / kSlots) & 1, &c.full[c2 % kSlots], (c2 / kSlots) & 1, &c.abort))
+          return;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int k = k3; k < k3 + 3; ++k, ++n.chunk) {
+          const uint32_t s = n.chunk % kSlots;
+          const uint64_t dk = dplus(dk0, s * kSlot);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          ptx::mma_ws_f16(d, dplus(dk, k * kChunk + ks * 32), dplus(dq, k * kChunk + ks * 32),
-                          kIdBf, (k | ks) != 0);
+          for (int ks = 0; ks < 4; ++ks)
+            ptx::mma_f16(d, dplus(dk, ks * 32), dplus(dq, k * kHalf + ks * 32), kIdBf,
+                         (k | ks) != 0);
+          ptx::mma_commit(&c.empty[s]);
+        }
+      }
+      ptx::mma_commit(&c.d_full[buf]);
+      ++n.part;
     }
-    ptx::mma_commit(&c.empty[s]);
-    ptx::mma_commit(&c.d_full[buf]);
     if (cur.last_of_segment()) ptx::mma_commit(&c.q_empty);
     ++n.tau;
     if (!cur.next(m.p, c)) break;
   }
 }
 
-// Weights of every other tile (tau % 2 == group): thread (q, i) of the group
-// holds cached row (32 q + i) % 64 for 32 of the heads.
+// Weights: thread (hh, row) sums heads [32 hh, 32 hh + 32) of the tile's row.
 template <int kDtype>
 __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t* base, int nseg,
-                                            uint32_t& tau, uint32_t& mine) {
+                                            Counts& n) {
   using S = Shape<kDtype>;
   const PartialParams& p = m.p;
-  const int group = threadIdx.x >> 7, t = threadIdx.x & 127;
-  const int row = t & 63, hh = t >> 6, lane = t & 31;
-  const uint32_t lane_base = c.tmem_base + ((uint32_t)((t >> 5) * 32) << 16);
+  const int hh = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t lane_base =
+      c.tmem_base + ((uint32_t)((row >> 5) * 32) << 16) + 32 * hh;
   const int hpq = p.heads / p.q_len;
   const float sl2 = p.scale * kLog2e;
-  int seg = -1;
-  TileCursor cur;
+  PairCursor cur;
   if (!cur.start(p, c, nseg)) return;
   while (true) {
-    if ((int)(tau & 1) == group) {
-      const uint32_t s = tau % S::kStages, buf = tau % kBufs;
-      const int b = cur.v.b;
-      if (cur.k != seg) {
-        // the readers of the old factors passed the group's last barrier
-        seg = cur.k;
-        if (t < 64) {
-          float2 f = make_float2(0.f, INFINITY);     // rows past the pass weigh nothing
-          if (t < p.heads) {
-            f.x = sl2;
-            if constexpr (kDtype == kKvFp8)
-              f.x *= __ldg(reinterpret_cast<const float*>(p.q_image + (size_t)b * kQImageBytes +
-                                                          S::kQBytes) + t);
-            const float l = __ldg(m.lse + (size_t)b * p.rows_o + t);
-            f.y = l == -INFINITY ? INFINITY : l * kLog2e;
-          }
-          c.head[group][t] = f;
+    const int b = cur.v.b;
+    if (cur.t == 0) {
+      // the readers of the old factors passed the last tile's barrier
+      if (threadIdx.x < 64) {
+        const int h = threadIdx.x;
+        float2 f = make_float2(0.f, INFINITY);     // rows past the pass weigh nothing
+        if (h < p.heads) {
+          f.x = sl2;
+          if constexpr (kDtype == kKvFp8)
+            f.x *= __ldg(reinterpret_cast<const float*>(p.q_image + (size_t)b * kQImageBytes +
+                                                        kQBytes) + h);
+          const float l = __ldg(m.lse + (size_t)b * p.rows_o + h);
+          f.y = l == -INFINITY ? INFINITY : l * kLog2e;
         }
-        ptx::named_bar(1 + group, kGroupThreads);
+        c.head[h] = f;
       }
-      const long long j = (long long)(cur.v.row_begin + cur.t * kTileRows) + row;
-      const int last = seq_len_of(p, b) - p.q_len;         // position of query 0
-      if (!ptx::mbar_wait(&c.full[s], (tau / S::kStages) & 1, &c.abort)) return;
-      const int nv = c.nv[s];
-      const bool live = row < nv && j < m.mass_stride;
-      float* o = m.mass + (size_t)b * m.mass_stride + j;
-      float old = 0.f;
-      if (hh == 0 && live && m.decay != 0.f) old = *o;
-      float sc[4] = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (kDtype == kKvFp8) {
-        const float4 v = *reinterpret_cast<const float4*>(base + S::kQBytes + s * S::kStageBytes +
-                                                          S::kScales + row * 16);
-        sc[0] = v.x;
-        sc[1] = v.y;
-        sc[2] = v.z;
-        sc[3] = v.w;
-      }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&c.empty[s]);
-      if (!ptx::mbar_wait(&c.d_full[buf], (tau / kBufs) & 1, &c.abort)) return;
+      ptx::named_bar(1, kWeightThreads);
+    }
+    const long long j = (long long)(cur.v.row_begin + cur.t * kTileMass) + row;
+    const int last = seq_len_of(p, b) - p.q_len;         // position of query 0
+    const uint32_t meta = n.tau % S::kMeta;
+    if (!ptx::mbar_wait(&c.meta[meta], (n.tau / S::kMeta) & 1, &c.abort)) return;
+    const bool in = (row & 63) < c.nv[meta][row >> 6];
+    const bool live = in && j < m.mass_stride;
+    float* o = m.mass + (size_t)b * m.mass_stride + j;
+    float old = 0.f;
+    if (hh == 0 && live && m.decay != 0.f) old = *o;
+    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (kDtype == kKvFp8) {
+      const float4 v =
+          *reinterpret_cast<const float4*>(base + kOffScale + meta * kScaleBytes + row * 16);
+      sc[0] = v.x;
+      sc[1] = v.y;
+      sc[2] = v.z;
+      sc[3] = v.w;
+    }
+    // heads below `from` belong to queries that do not see the row
+    const int pos = (int)j * p.nshards + p.shard;
+    const int from = p.q_len > 1 && in ? max(0, pos - last) * hpq : 0;
+    const bool masked = __any_sync(0xffffffffu, from > 0);
+    float v[32], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < S::kParts; ++k) {
+      const uint32_t buf = n.part % kBufs;
+      if (!ptx::mbar_wait(&c.d_full[buf], (n.part / kBufs) & 1, &c.abort)) return;
       __syncwarp();
       ptx::tc_fence_after();
-      // heads below `from` belong to queries that do not see the row
-      const int pos = (int)j * p.nshards + p.shard;
-      const int from = p.q_len > 1 && row < nv ? max(0, pos - last) * hpq : 0;
-      const bool masked = __any_sync(0xffffffffu, from > 0);
-      float sum = 0.f;
+      uint32_t x[32];
+      ptx::tmem_ld32(lane_base + 64 * buf, x);
+      ptx::tmem_wait_ld();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.d_empty[buf]);
+      ++n.part;
+      if (k < S::kParts - 1) {
 #pragma unroll
-      for (int piece = 0; piece < 2; ++piece) {
-        const int h0 = 32 * hh + 16 * piece;
-        uint32_t x[S::kParts][16];
+        for (int e = 0; e < 32; ++e)
+          v[e] = k == 0 ? sc[0] * __uint_as_float(x[e]) : fmaf(sc[k & 3], __uint_as_float(x[e]), v[e]);
+      } else {
 #pragma unroll
-        for (int k = 0; k < S::kParts; ++k)
-          ptx::tmem_ld16(lane_base + buf * (32 * S::kParts) + 32 * k + 16 * piece, x[k]);
-        ptx::tmem_wait_ld();
-        if (piece == 1) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&c.d_empty[buf]);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 f = c.head[group][h0 + e];
-          float y;
-          if constexpr (kDtype == kKvFp8) {
-            float v = sc[0] * __uint_as_float(x[0][e]);
-            v = fmaf(sc[1], __uint_as_float(x[1][e]), v);
-            v = fmaf(sc[2], __uint_as_float(x[2][e]), v);
-            v = fmaf(sc[3], __uint_as_float(x[3][e]), v);
-            y = fmaf(f.x, v, fmaf(sl2, __uint_as_float(x[4][e]), -f.y));
-          } else {
-            y = fmaf(f.x, __uint_as_float(x[0][e]), -f.y);
-          }
+        for (int e = 0; e < 32; ++e) {
+          const float2 f = c.head[32 * hh + e];
+          const float y = S::kParts > 1
+                              ? fmaf(f.x, v[e], fmaf(sl2, __uint_as_float(x[e]), -f.y))
+                              : fmaf(f.x, __uint_as_float(x[e]), -f.y);
           float w = ex2(y);
-          if (masked && h0 + e < from) w = 0.f;
+          if (masked && 32 * hh + e < from) w = 0.f;
           sum += w;
         }
       }
-      float* half = c.half[group][mine & 1];
-      if (hh == 1) half[row] = sum;
-      ptx::named_bar(1 + group, kGroupThreads);
-      if (hh == 0) {
-        const float add = sum + half[row];
-        if (live) *o = m.decay == 0.f ? add : fmaf(m.decay, old, add);
-        if (row < nv && !live && p.flags) atomicOr(p.flags, kFlagBadLength);
-      }
-      ++mine;
     }
-    ++tau;
+    float* half = c.half[n.tau & 1];
+    if (hh == 1) half[row] = sum;
+    ptx::named_bar(1, kWeightThreads);
+    if (hh == 0) {
+      const float add = sum + half[row];
+      if (live) *o = m.decay == 0.f ? add : fmaf(m.decay, old, add);
+      if (in && !live && p.flags) atomicOr(p.flags, kFlagBadLength);
+    }
+    ++n.tau;
     if (!cur.next(p, c)) break;
+  }
+}
+
+// Uses of ring entry i after n uses in all of a ring of `size`, and a wait for
+// the last of them.
+__device__ __forceinline__ void drain(uint64_t* ring, int size, uint32_t n, Ctl& c) {
+  for (uint32_t i = 0; i < (uint32_t)size; ++i) {
+    const uint32_t u = n > i ? (n - i + size - 1) / size : 0;
+    if (u > 0) ptx::mbar_wait(&ring[i], (u - 1) & 1, &c.abort);
   }
 }
 
@@ -336,21 +436,21 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  Ctl& c = *reinterpret_cast<Ctl*>(base + S::kQBytes + S::kStages * S::kStageBytes);
+  Ctl& c = *reinterpret_cast<Ctl*>(base + ctl_offset<kDtype>());
   const PartialParams& p = m.p;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       ptx::mbar_init(&c.full[s], 1);
-      // the MMAs' commit and the four warps that read the row count and scales
-      ptx::mbar_init(&c.empty[s], 5);
+      ptx::mbar_init(&c.empty[s], 1);
     }
     for (int k = 0; k < kBufs; ++k) {
       ptx::mbar_init(&c.d_full[k], 1);
-      ptx::mbar_init(&c.d_empty[k], 4);
+      ptx::mbar_init(&c.d_empty[k], kWeightThreads / 32);
     }
+    for (int k = 0; k < S::kMeta; ++k) ptx::mbar_init(&c.meta[k], 1);
     ptx::mbar_init(&c.q_full, 1);
-    ptx::mbar_init(&c.q_empty, 1);
+    ptx::mbar_init(&c.q_empty, S::kIssuers);
     c.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -360,48 +460,40 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   __syncthreads();
   ptx::tc_fence_after();
   const int T = total_tiles(p, c.warp_sums);
-  const int tpc = T > 0 ? (T + p.num_ctas - 1) / p.num_ctas : 0;
-  const int lo = blockIdx.x * tpc, hi = min(T, lo + tpc);
+  // an even number of blocks a CTA, so that few tiles are half empty
+  int tpc = T > 0 ? (T + p.num_ctas - 1) / p.num_ctas : 0;
+  tpc += tpc & 1;
+  const int lo = min((long long)T, (long long)blockIdx.x * tpc), hi = min(T, lo + tpc);
   Counts n;
-  uint32_t tau = 0, mine = 0;
   int first = 0;
   while (lo < hi) {
     const int total = collect_segments_n(p, lo, hi, first, kMaxSeg, c);
     const int nseg = min(kMaxSeg, total - first);
     if (nseg <= 0) break;
     if (warp < kLoadWarp) {
-      weight_role<kDtype>(m, c, base, nseg, tau, mine);
+      weight_role<kDtype>(m, c, base, nseg, n);
     } else if (warp == kLoadWarp) {
       if ((threadIdx.x & 31) == 0) load_role<kDtype>(m, c, base, nseg, n);
     } else {
-      if ((threadIdx.x & 31) == 0) mma_role<kDtype>(m, c, base, nseg, n);
+      if ((threadIdx.x & 31) == 0 && warp < kMmaWarp + S::kIssuers)
+        mma_role<kDtype>(m, c, base, nseg, warp - kMmaWarp, n);
     }
     __syncthreads();
     if (c.abort) break;
     first += kMaxSeg;
     if (total <= first) break;
   }
-  // Drain: every asynchronous arrival lands before the CTA exits.  The waits
-  // are for the latest phase of each barrier (after a timeout: bounded).
-  if (threadIdx.x == kMmaWarp * 32) {
-    for (uint32_t s = 0; s < (uint32_t)S::kStages; ++s) {
-      const uint32_t u = n.tau > s ? (n.tau - s + S::kStages - 1) / S::kStages : 0;
-      if (u > 0) ptx::mbar_wait(&c.empty[s], (u - 1) & 1, &c.abort);
-    }
-    for (uint32_t k = 0; k < (uint32_t)kBufs; ++k) {
-      const uint32_t u = n.tau > k ? (n.tau - k + kBufs - 1) / kBufs : 0;
-      if (u > 0) ptx::mbar_wait(&c.d_full[k], (u - 1) & 1, &c.abort);
-    }
+  // Drain: every asynchronous arrival lands before the CTA exits (after a
+  // timeout these waits are bounded too).
+  if ((threadIdx.x & 31) == 0 && warp >= kMmaWarp && warp < kMmaWarp + S::kIssuers) {
+    drain(c.empty, kSlots, n.chunk, c);
+    drain(c.d_full, kBufs, n.part, c);
+    if (n.sigma > 0) ptx::mbar_wait(&c.q_empty, (n.sigma - 1) & 1, &c.abort);
   }
   if (threadIdx.x == kLoadWarp * 32) {
-    for (uint32_t s = 0; s < (uint32_t)S::kStages; ++s) {
-      const uint32_t u = n.tau > s ? (n.tau - s + S::kStages - 1) / S::kStages : 0;
-      if (u > 0) ptx::mbar_wait(&c.full[s], (u - 1) & 1, &c.abort);
-    }
-    if (n.sigma > 0) {
-      ptx::mbar_wait(&c.q_full, (n.sigma - 1) & 1, &c.abort);
-      ptx::mbar_wait(&c.q_empty, (n.sigma - 1) & 1, &c.abort);
-    }
+    drain(c.full, kSlots, n.chunk, c);
+    drain(c.meta, S::kMeta, n.tau, c);
+    if (n.sigma > 0) ptx::mbar_wait(&c.q_full, (n.sigma - 1) & 1, &c.abort);
   }
   ptx::tc_fence_before();
   __syncthreads();
