@@ -50,7 +50,7 @@ struct SelectParams {
   int topk, sink, recent;
   int tiles;                   // scoring tiles per row (from the table's stride)
   uint8_t* q_codes;            // [rows][kQBytes]
-  int num_ctas;                // of the scoring kernel
+  int num_ctas;                // SMs
   float* scores;               // [rows][tiles][heads][kTile]
   uint32_t* tile_max;          // [rows][tiles][heads], as ordered keys
   int* out_blocks;             // [rows][topk] or nullptr
@@ -182,6 +182,13 @@ struct TileWalk {
   }
 };
 
+// fp32 of a whole number below 2^22 in magnitude (a group's products stay below
+// 2^21): added to the bits of 1.5 * 2^23 it lands in the mantissa.  Two plain
+// operations; the conversion instruction runs at a quarter of their rate.
+__device__ __forceinline__ float small_int(uint32_t x) {
+  return __fsub_rn(__uint_as_float(0x4B400000u + x), 12582912.f);
+}
+
 // Copies of every tile (four warps) and of each row's query image.
 __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, uint8_t* base, int r0,
                                           int lo, int hi, uint32_t& tau, uint32_t& sigma) {
@@ -189,24 +196,36 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
   TileWalk w;
   if (!w.start(c, lo, hi)) return;
   bool fresh = true;
+  const int un0 = t & 15;
+  // the tile's table entries, loaded a tile ahead: the copies of a tile would
+  // otherwise wait for eight of them one after the other
+  int ids[8];
+  auto entries = [&]() {
+    const int* table =
+        p.block_table + (size_t)((r0 + w.row) / p.q_len) * p.bt_stride + w.tile * kTile;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = (t >> 4) + 8 * k;
+      ids[k] = w.tile * kTile + row < w.nb ? __ldg(table + row) : 0;
+    }
+  };
+  entries();
   while (true) {
     const uint32_t s = tau % kScoreStages;
     if (tau >= (uint32_t)kScoreStages &&
         !ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort))
       return;
     const int r = r0 + w.row;
-    const int* table = p.block_table + (size_t)(r / p.q_len) * p.bt_stride + w.tile * kTile;
     uint8_t* stage = base + kOffStage + s * kStageBytes;
     const uint32_t dst = ptx::smem_addr(stage);
     const int n = min(kTile, w.nb - w.tile * kTile);
     // sixteen lanes take a row's 38 pieces; rows past the tile's end are left
     // as they are (they only reach their own lanes)
-    const int un0 = t & 15;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int row = (t >> 4) + 8 * k;
       if (row < n) {
-        int blk = __ldg(table + row);
+        int blk = ids[k];
         if (blk < 0 || (long long)blk >= p.num_blocks) {
           if (un0 == 0 && p.flags) atomicOr(p.flags, kFlagBadBlock);
           blk = 0;
@@ -236,6 +255,7 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
     fresh = w.last_of_row();
     ++tau;
     if (!w.next(c)) break;
+    entries();
   }
 }
 
@@ -293,18 +313,18 @@ __device__ __forceinline__ void score_role(const SelectParams& p, ScoreCtl& c, u
     fresh = w.last_of_row();
     if ((int)(tau & 1) == group) {
       const uint32_t s = tau % kScoreStages, buf = tau % kBufs;
-      if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
-      const uint8_t* sp = base + kOffStage + s * kStageBytes + kGroups * kChunk + row * 32;
-      const float4 s4 = *reinterpret_cast<const float4*>(sp);
-      const float sc[kGroups] = {s4.x, s4.y, s4.z, s4.w, *reinterpret_cast<const float*>(sp + 16)};
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&c.empty[s]);
       const int r = r0 + w.row, k = w.tile * kTile + row;
       bool live = k < w.nb;
       if (live) {
         const int blk = __ldg(p.block_table + (size_t)(r / p.q_len) * p.bt_stride + k);
         live = blk >= 0 && (long long)blk < p.num_blocks;
       }
+      if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
+      const uint8_t* sp = base + kOffStage + s * kStageBytes + kGroups * kChunk + row * 32;
+      const float4 s4 = *reinterpret_cast<const float4*>(sp);
+      const float sc[kGroups] = {s4.x, s4.y, s4.z, s4.w, *reinterpret_cast<const float*>(sp + 16)};
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.empty[s]);
       if (!ptx::mbar_wait(&c.d_full[buf], (tau / kBufs) & 1, &c.abort)) return;
       __syncwarp();
       ptx::tc_fence_after();
@@ -331,7 +351,7 @@ __device__ __forceinline__ void score_role(const SelectParams& p, ScoreCtl& c, u
             float v = 0.f;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-              const float term = __fmul_rn((float)(int)x[g][e], __fmul_rn(qs[g], sc[g]));
+              const float term = __fmul_rn(small_int(x[g][e]), __fmul_rn(qs[g], sc[g]));
               v = g == 0 ? term : __fadd_rn(v, term);
             }
             if (!live) v = -INFINITY;
@@ -441,7 +461,7 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   extern __shared__ __align__(16) uint32_t dyn[];
   __shared__ topk::Ctl c;
   __shared__ float hmax[64];
-  __shared__ int s_pos;
+  __shared__ uint32_t kmax[64];
   topk::cg::cluster_group cl = topk::cg::this_cluster();
   const int r = blockIdx.y, b = r / p.q_len;
   int nb;
@@ -452,49 +472,61 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   topk::slice(nb, cl.block_rank(), cl.num_blocks(), &lo, &hi);
   const int want = min(nb, p.topk);
   const int tiles = (nb + kTile - 1) / kTile;
-  if (threadIdx.x < p.heads) {
+  if (threadIdx.x < 64) kmax[threadIdx.x] = 0;
+  __syncthreads();
+  {
+    const uint32_t* tm = p.tile_max + (size_t)r * p.tiles * p.heads;
+    const int h = threadIdx.x & 63, t0 = threadIdx.x >> 6;
     uint32_t m = 0;
-    for (int t = 0; t < tiles; ++t)
-      m = max(m, p.tile_max[((size_t)r * p.tiles + t) * p.heads + threadIdx.x]);
-    hmax[threadIdx.x] = topk::value_of(m);
+    if (h < p.heads) {
+#pragma unroll 4
+      for (int t = t0; t < tiles; t += topk::kThreads / 64) m = max(m, __ldg(tm + t * p.heads + h));
+      atomicMax(&kmax[h], m);
+    }
   }
+  __syncthreads();
+  if (threadIdx.x < 64) hmax[threadIdx.x] = topk::value_of(kmax[threadIdx.x]);
   __syncthreads();
   for (int k = lo + threadIdx.x; k < hi; k += topk::kThreads) {
     uint32_t key = 0xFFFFFFFFu;
     if (k >= p.sink && k < nb - p.recent) {
       const float* s = p.scores + ((size_t)r * p.tiles + k / kTile) * p.heads * kTile + k % kTile;
       float rank = -INFINITY;
-      for (int h = 0; h < p.heads; ++h) {
-        const float v = s[h * kTile];
+      auto add = [&](float v, int h) {
         // equal infinities: no distance
         rank = fmaxf(rank, v == hmax[h] ? 0.f : __fsub_rn(v, hmax[h]));
+      };
+      int h = 0;
+      for (; h + 16 <= p.heads; h += 16) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __ldg(s + (h + e) * kTile);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) add(v[e], h + e);
       }
+      for (; h < p.heads; ++h) add(__ldg(s + h * kTile), h);
       key = topk::key_of(rank);
     }
     keys[k - lo] = key;
   }
   __syncthreads();
   if (want > 0)
-    topk::mark(cl, c, lo, hi, want, bits, [&](int i) { return keys[i - lo]; });
+    topk::mark(cl, c, lo, hi, want, bits, [&](int i, bool) { return keys[i - lo]; });
   // places of this slice's blocks in the list
-  int mine = 0;
-  for (int w = threadIdx.x; w < (hi - lo + 31) / 32; w += topk::kThreads) mine += __popc(bits[w]);
-  int tot;
-  block_exclusive_scan(mine, c.warp_sums, &tot);
-  if (threadIdx.x == 0) c.share[0] = tot;
-  cl.sync();
-  int pos = topk::before(cl, c, 0);
-  cl.sync();          // shared memory stays until every CTA has read it
-  for (int base = lo; base < hi; base += topk::kThreads) {
-    const int k = base + threadIdx.x;
-    const bool take = k < hi && ((bits[(k - lo) >> 5] >> ((k - lo) & 31)) & 1u);
-    const int at = pos + block_exclusive_scan(take ? 1 : 0, c.warp_sums, &tot);
-    pos += tot;
-    if (take) {
-      if (p.out_blocks) p.out_blocks[(size_t)r * p.topk + at] = k;
-      p.out_table[(size_t)r * p.topk + at] = __ldg(p.block_table + (size_t)b * p.bt_stride + k);
-    }
+  int pos[1] = {0};
+  if (cl.num_blocks() > 1) {
+    int mine = 0, tot;
+    for (int w = threadIdx.x; w < (hi - lo + 31) / 32; w += topk::kThreads) mine += __popc(bits[w]);
+    block_exclusive_scan(mine, c.warp_sums, &tot);
+    if (threadIdx.x == 0) c.share[0] = tot;
+    topk::sync(cl);
+    pos[0] = topk::before(cl, c, 0);
+    topk::sync(cl);          // shared memory stays until every CTA has read it
   }
+  topk::emit<1>(c, lo, hi, pos, [&](int, int w) { return bits[w]; }, [&](int, int k, int at) {
+    if (p.out_blocks) p.out_blocks[(size_t)r * p.topk + at] = k;
+    p.out_table[(size_t)r * p.topk + at] = __ldg(p.block_table + (size_t)b * p.bt_stride + k);
+  });
   if (cl.block_rank() == 0) {
     for (int i = want + threadIdx.x; i < p.topk; i += topk::kThreads) {
       if (p.out_blocks) p.out_blocks[(size_t)r * p.topk + i] = -1;
@@ -523,8 +555,8 @@ SelectLayout layout(int rows, int heads, int stride) {
 }
 
 // Largest table stride: a row's keys and bits fit one cluster's shared memory.
-constexpr int kMaxCluster = 8;
-constexpr int kMaxStride = kMaxCluster * 49152;
+constexpr int kMaxKeys = 49152;            // of a CTA
+constexpr int kMaxStride = topk::kMaxCluster * kMaxKeys;
 
 int check_sizes(int batch, int heads, int q_len, int stride) {
   if (batch < 0 || heads < 1 || q_len < 1 || q_len > kMaxQueryLen || stride < 1)
@@ -596,8 +628,9 @@ int check_select(const SelectArgs& a, SelectParams* p) {
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   const int rows = p.batch * p.q_len;
   q_codes_kernel<<<dim3(rows, 64), 160, 0, st>>>(p);
-  score_kernel<<<p.num_ctas, kScoreThreads, kScoreSmem, st>>>(p);
-  const int size = p.bt_stride <= 4096 ? 1 : kMaxCluster;
+  score_kernel<<<(int)std::min<long long>(p.num_ctas, (long long)rows * p.tiles), kScoreThreads, kScoreSmem, st>>>(p);
+  int size = topk::cluster_size(p.bt_stride, rows, p.num_ctas);
+  while ((long long)size * kMaxKeys < p.bt_stride) size *= 2;      // keys and bits in shared memory
   const int words = topk::slice_words(p.bt_stride, size);
   return topk::launch(choose_kernel, rows, size, (size_t)words * 33 * 4, st, p, words);
 }
@@ -610,7 +643,6 @@ int run_select(SelectParams& p, uint8_t* ws, cudaStream_t st) {
   if (prepare_device(dev) != cudaSuccess) return DCPMLA_ERR_CUDA;
   int rc = dcpmla_device_sm_count(&p.num_ctas);
   if (rc != DCPMLA_OK) return rc;
-  p.num_ctas = (int)std::min<long long>(p.num_ctas, (long long)p.batch * p.q_len * p.tiles);
   const SelectLayout l = layout(p.batch * p.q_len, p.heads, p.bt_stride);
   p.q_codes = ws + l.q_codes;
   p.scores = reinterpret_cast<float*>(ws + l.scores);

@@ -28,7 +28,6 @@ namespace {
 
 struct EvictParams {
   uint8_t* kv;
-  int row_bytes;
   long long num_blocks;
   const int* block_table;
   int bt_stride;
@@ -94,80 +93,92 @@ __global__ void __launch_bounds__(topk::kThreads) pick_kernel(const EvictParams 
     return;
   }
   const int fresh = L - p.recent;    // positions from here on are recent
-  topk::mark(cl, c, lo, hi, keep, bits, [&](int j) {
+  const bool put_mass = p.mass_out != p.mass;
+  const bool put_pos = p.positions_out && p.positions_out != p.positions;
+  topk::mark(cl, c, lo, hi, keep, bits, [&](int j, bool first) {
     const int t = position_of(p, base, j);
-    return t < p.sink || t >= fresh ? 0xFFFFFFFFu : topk::key_of(p.mass[base + j]);
+    const float m = p.mass[base + j];
+    if (first && j < p.budget) {
+      // as if the row stayed; the move kernel corrects the freed places
+      if (put_mass) p.mass_out[base + j] = m;
+      if (put_pos) p.positions_out[base + j] = t;
+    }
+    return t < p.sink || t >= fresh ? 0xFFFFFFFFu : topk::key_of(m);
   });
   // Freed places (below the budget, not taken) and moving rows (taken, at or
   // past it) of this slice; every mass has been read by now.
-  int holes = 0, movers = 0;
-  for (int w = threadIdx.x; w < (hi - lo + 31) / 32; w += topk::kThreads) {
+  auto word = [&](int list, int w) {
     const int j0 = lo + 32 * w;
     const uint32_t live = hi - j0 >= 32 ? 0xFFFFFFFFu : (1u << (hi - j0)) - 1u;
     const int d = p.budget - j0;     // rows of this word below the budget
     const uint32_t below = d >= 32 ? 0xFFFFFFFFu : d <= 0 ? 0u : (1u << d) - 1u;
-    holes += __popc(~bits[w] & live & below);
-    movers += __popc(bits[w] & live & ~below);
-  }
-  int th, tm;
-  block_exclusive_scan(holes, c.warp_sums, &th);
-  block_exclusive_scan(movers, c.warp_sums, &tm);
-  if (threadIdx.x == 0) {
-    c.share[0] = th;
-    c.share[1] = tm;
-  }
-  cl.sync();
-  int ph = topk::before(cl, c, 0), pm = topk::before(cl, c, 1);
-  if (cl.block_rank() == cl.num_blocks() - 1 && threadIdx.x == 0) p.count[b] = pm + tm;
-  for (int j0 = lo; j0 < hi; j0 += topk::kThreads) {
-    const int j = j0 + threadIdx.x;
-    const bool in = j < hi;
-    const bool taken = in && ((bits[(j - lo) >> 5] >> ((j - lo) & 31)) & 1u);
-    const bool hole = in && !taken && j < p.budget, mover = taken && j >= p.budget;
-    int t1, t2;
-    const int ih = ph + block_exclusive_scan(hole ? 1 : 0, c.warp_sums, &t1);
-    const int im = pm + block_exclusive_scan(mover ? 1 : 0, c.warp_sums, &t2);
-    ph += t1;
-    pm += t2;
-    if (hole) p.holes[(size_t)b * p.budget + ih] = j;
-    if (mover) p.movers[(size_t)b * p.budget + im] = j;
-    if (taken && !mover) {
-      if (p.mass_out != p.mass) p.mass_out[base + j] = p.mass[base + j];
-      if (p.positions_out && p.positions_out != p.positions)
-        p.positions_out[base + j] = position_of(p, base, j);
+    return list == 0 ? ~bits[w] & live & below : bits[w] & live & ~below;
+  };
+  int pos[2] = {0, 0};
+  if (cl.num_blocks() > 1) {
+    int holes = 0, movers = 0, th, tm;
+    for (int w = threadIdx.x; w < (hi - lo + 31) / 32; w += topk::kThreads) {
+      holes += __popc(word(0, w));
+      movers += __popc(word(1, w));
     }
+    block_exclusive_scan(holes, c.warp_sums, &th);
+    block_exclusive_scan(movers, c.warp_sums, &tm);
+    if (threadIdx.x == 0) {
+      c.share[0] = th;
+      c.share[1] = tm;
+    }
+    topk::sync(cl);
+    pos[0] = topk::before(cl, c, 0);
+    pos[1] = topk::before(cl, c, 1);
+    topk::sync(cl);      // shared memory stays until every CTA has read it
   }
-  cl.sync();      // shared memory stays until every CTA has read it
+  topk::emit<2>(c, lo, hi, pos, word, [&](int list, int j, int at) {
+    (list == 0 ? p.holes : p.movers)[(size_t)b * p.budget + at] = j;
+  });
+  if (cl.block_rank() == cl.num_blocks() - 1 && threadIdx.x == 0) p.count[b] = pos[1];
 }
 
 // Physical row address, or nullptr (flagged) for a table entry outside the pool.
+template <int kRowBytes>
 __device__ __forceinline__ uint8_t* row_at(const EvictParams& p, int b, int j) {
   const int blk = __ldg(p.block_table + (size_t)b * p.bt_stride + j / kBlock);
   if (blk < 0 || (long long)blk >= p.num_blocks) {
-    if (p.flags && (threadIdx.x & 31) == 0) atomicOr(p.flags, kFlagBadBlock);
+    if (p.flags) atomicOr(p.flags, kFlagBadBlock);
     return nullptr;
   }
-  return p.kv + ((size_t)blk * kBlock + j % kBlock) * p.row_bytes;
+  return p.kv + ((size_t)blk * kBlock + j % kBlock) * kRowBytes;
 }
 
 constexpr int kMoveWarps = 8;
+constexpr int kMoveRows = 4;       // rows a warp copies at once, eight lanes each
 
-// One warp per moving row: its bytes, its mass and its position.
+// Moving rows: the bytes, the mass and the position.  A row's copy starts with
+// three dependent loads (place, table entry, row), so a warp takes four rows at
+// once, all of their bytes in flight before the first store.
+template <int kRowBytes>
 __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictParams p) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  constexpr int kUnits = kRowBytes / 16, kPer = (kUnits + 7) / 8;
+  const int b = blockIdx.y, sub = (threadIdx.x & 31) >> 3, l = threadIdx.x & 7;
   const int n = __ldg(p.count + b);
   const size_t base = (size_t)b * p.mass_stride;
-  for (int i = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); i < n; i += gridDim.x * kMoveWarps) {
+  const int stride = gridDim.x * kMoveWarps * kMoveRows;
+  for (int i = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * kMoveRows + sub; i < n; i += stride) {
     const int src = __ldg(p.movers + (size_t)b * p.budget + i);
     const int dst = __ldg(p.holes + (size_t)b * p.budget + i);
-    if (lane == 0) {
+    const uint4* s = reinterpret_cast<const uint4*>(row_at<kRowBytes>(p, b, src));
+    uint4* d = reinterpret_cast<uint4*>(row_at<kRowBytes>(p, b, dst));
+    if (l == 0) {
       p.mass_out[base + dst] = p.mass[base + src];
       if (p.positions_out) p.positions_out[base + dst] = position_of(p, base, src);
     }
-    const uint4* s = reinterpret_cast<const uint4*>(row_at(p, b, src));
-    uint4* d = reinterpret_cast<uint4*>(row_at(p, b, dst));
     if (!s || !d) continue;
-    for (int u = lane; u < p.row_bytes / 16; u += 32) d[u] = s[u];
+    uint4 v[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (l + 8 * k < kUnits) v[k] = s[l + 8 * k];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (l + 8 * k < kUnits) d[l + 8 * k] = v[k];
   }
 }
 
@@ -179,7 +190,6 @@ size_t evict_bytes(int batch, int budget) {
   return kWsHeader + round256((size_t)batch * 4) + 2 * round256((size_t)batch * budget * 4);
 }
 
-constexpr int kMaxCluster = 8;
 constexpr long long kMaxRows = 8ll << 20;     // rows of a request: a bit each in the cluster
 
 std::mutex g_mutex;
@@ -223,7 +233,6 @@ int mla_cache_evict(void* kv_cache, int kv_dtype, int64_t num_blocks, int block_
   if (cudaGetDevice(&dev) != cudaSuccess) return DCPMLA_ERR_CUDA;
   EvictParams p{};
   p.kv = static_cast<uint8_t*>(kv_cache);
-  p.row_bytes = kv_dtype == DCPMLA_KV_BF16 ? kRowBytesBf16 : kRowBytesFp8;
   p.num_blocks = num_blocks;
   p.block_table = block_table;
   p.bt_stride = block_table_stride;
@@ -250,20 +259,26 @@ int mla_cache_evict(void* kv_cache, int kv_dtype, int64_t num_blocks, int block_
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!g_done[dev]) {
       if (cudaFuncSetAttribute(pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(kMaxRows / kMaxCluster / 8 + 256)) != cudaSuccess)
+                               (int)(kMaxRows / topk::kMaxCluster / 8 + 256)) != cudaSuccess)
         return DCPMLA_ERR_CUDA;
       g_done[dev] = true;
     }
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long most = std::min<long long>((long long)block_table_stride * kBlock, mass_stride);
-  const int size = most <= 8192 ? 1 : kMaxCluster;
+  int size = topk::cluster_size(most, batch, sms);
+  while ((most + size - 1) / size > kMaxRows / topk::kMaxCluster) size *= 2;   // bits in shared memory
   const size_t smem = (size_t)topk::slice_words(most, size) * 4;
   if (topk::launch(pick_kernel, batch, size, smem, st, p) != cudaSuccess) return DCPMLA_ERR_CUDA;
   const int most_moves = (int)std::min<long long>(budget, std::max<long long>(most - budget, 0));
   if (most_moves > 0) {
-    const int gx = std::max(1, std::min((most_moves + kMoveWarps - 1) / kMoveWarps, sms * 8 / batch));
-    move_kernel<<<dim3(gx, batch), 32 * kMoveWarps, 0, st>>>(p);
+    constexpr int kCtaRows = kMoveWarps * kMoveRows;
+    const int gx = std::max(1, std::min((most_moves + kCtaRows - 1) / kCtaRows, sms * 8 / batch));
+    const dim3 grid(gx, batch);
+    if (kv_dtype == DCPMLA_KV_BF16)
+      move_kernel<kRowBytesBf16><<<grid, 32 * kMoveWarps, 0, st>>>(p);
+    else
+      move_kernel<kRowBytesFp8><<<grid, 32 * kMoveWarps, 0, st>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? DCPMLA_OK : DCPMLA_ERR_CUDA;
 }

@@ -21,14 +21,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) dcp_merge_kernel(
              out + (size_t)row * kVDim, out_lse ? out_lse + row : nullptr);
 }
 
-// Combine of the split pieces of each request.  Grid: one CTA per
-// (request, group of 8 heads), one warp per head.
+// Combine of the split pieces of each request.  Grid: one CTA per (request,
+// group of 8 / kParts heads), kParts warps per head.
+template <int kParts>
 __global__ void __launch_bounds__(256) split_combine_kernel(PartialParams p) {
   __shared__ int warp_sums[8];
   __shared__ int sh_start, sh_nt;
-  const int hgroups = (p.heads + 7) / 8;
+  constexpr int kHeads = 8 / kParts;
+  const int hgroups = (p.heads + kHeads - 1) / kHeads;
   const int b = blockIdx.x / hgroups;
-  const int h = (blockIdx.x % hgroups) * 8 + (threadIdx.x >> 5);
+  const int part = (threadIdx.x >> 5) % kParts;
+  const int h = (blockIdx.x % hgroups) * kHeads + (threadIdx.x >> 5) / kParts;
   int first_slot, count;
   if (p.sparse_idx) {
     if (p.sparse_parts == 1) return;          // written directly by the partial kernel
@@ -55,7 +58,7 @@ __global__ void __launch_bounds__(256) split_combine_kernel(PartialParams p) {
       if (h < p.heads) {
         float* o = p.out + ((size_t)b * p.rows_o + h) * kVDim;
         for (int i = threadIdx.x & 31; i < kVDim; i += 32) o[i] = 0.f;
-        if ((threadIdx.x & 31) == 0) p.out_lse[(size_t)b * p.rows_o + h] = -CUDART_INF_F;
+        if ((threadIdx.x & 31) == 0 && part == 0) p.out_lse[(size_t)b * p.rows_o + h] = -CUDART_INF_F;
       }
       return;
     }
@@ -66,9 +69,9 @@ __global__ void __launch_bounds__(256) split_combine_kernel(PartialParams p) {
     count = c_last - c_first + 1;
   }
   if (h < p.heads)
-    merge_warp(StridedPieces{p.ws_o, p.ws_lse, (size_t)first_slot * p.heads + h, (size_t)p.heads},
-               count, p.out + ((size_t)b * p.rows_o + h) * kVDim,
-               p.out_lse + (size_t)b * p.rows_o + h);
+    merge_warp<kParts>(
+        StridedPieces{p.ws_o, p.ws_lse, (size_t)first_slot * p.heads + h, (size_t)p.heads}, count,
+        p.out + ((size_t)b * p.rows_o + h) * kVDim, p.out_lse + (size_t)b * p.rows_o + h, part);
 }
 
 }  // namespace
@@ -84,8 +87,13 @@ cudaError_t launch_dcp_merge(const float* partials, const float* lses, int num_s
 
 cudaError_t launch_split_combine(const PartialParams& p, cudaStream_t st) {
   if ((p.sparse_idx && p.sparse_parts == 1) || p.request_aligned) return cudaSuccess;
-  const int hgroups = (p.heads + 7) / 8;
-  split_combine_kernel<<<p.batch * hgroups, 256, 0, st>>>(p);
+  // few requests have many pieces each and few heads to spread them over: four
+  // warps a head then (measured at one request: 42 -> 6 us); with many, the
+  // CTAs' common look at the lengths costs more than it gains
+  if ((long long)p.batch * p.heads <= 1024)
+    split_combine_kernel<4><<<p.batch * ((p.heads + 1) / 2), 256, 0, st>>>(p);
+  else
+    split_combine_kernel<1><<<p.batch * ((p.heads + 7) / 8), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -43,48 +43,71 @@ struct TablePieces {
 };
 
 // One warp merges `count` pieces of one row into out_o (512 floats, 16-byte
-// aligned) and *out_lse (if not null).
-template <class Pieces>
+// aligned) and *out_lse (if not null): all of it, or columns [128 part, 128
+// part + 128) with kParts = 4 (part 0 writes the LSE).  The pieces are added in
+// order whatever the batch: a batch only has their loads in flight together
+// (64 pieces of one request's 64 heads, one after the other: 42 us).
+template <int kParts = 1, class Pieces>
 __device__ __forceinline__ void merge_warp(const Pieces& pc, int count, float* __restrict__ out_o,
-                                           float* __restrict__ out_lse) {
+                                           float* __restrict__ out_lse, int part = 0) {
+  constexpr int kVec = 4 / kParts;               // float4 per lane
+  constexpr int kBatch = kParts == 1 ? 4 : 16;   // pieces with loads in flight
   const int lane = threadIdx.x & 31;
+  const int col = part * 32 + lane;
   float M = -CUDART_INF_F;
   for (int k = lane; k < count; k += 32) M = fmaxf(M, pc.lse_of(k));
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-  float4 acc[4];
+  float4 acc[kVec];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kVec; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (M == -CUDART_INF_F) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(out_o)[i * 32 + lane] = acc[i];
-    if (lane == 0 && out_lse) *out_lse = -CUDART_INF_F;
+    for (int i = 0; i < kVec; ++i) reinterpret_cast<float4*>(out_o)[i * 32 + col] = acc[i];
+    if (lane == 0 && out_lse && part == 0) *out_lse = -CUDART_INF_F;
     return;
   }
   float wsum = 0.f;
-  for (int k = 0; k < count; ++k) {
-    const float lk = pc.lse_of(k);
-    if (lk == -CUDART_INF_F) continue;
-    const float w = expf(lk - M);
-    wsum += w;
-    const float4* src = pc.row(k);
+  for (int k0 = 0; k0 < count; k0 += 32) {
+    const float mine = k0 + lane < count ? pc.lse_of(k0 + lane) : -CUDART_INF_F;
+    const int n = min(32, count - k0);
+    for (int j0 = 0; j0 < n; j0 += kBatch) {
+      float lk[kBatch];
+      float4 v[kBatch][kVec];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(src + i * 32 + lane);
-      acc[i].x = fmaf(w, v.x, acc[i].x);
-      acc[i].y = fmaf(w, v.y, acc[i].y);
-      acc[i].z = fmaf(w, v.z, acc[i].z);
-      acc[i].w = fmaf(w, v.w, acc[i].w);
+      for (int j = 0; j < kBatch; ++j) {
+        // past the end: the lane holds -inf
+        lk[j] = __shfl_sync(0xffffffffu, mine, (j0 + j) & 31);
+        if (j0 + j >= n) lk[j] = -CUDART_INF_F;
+        if (lk[j] != -CUDART_INF_F) {
+          const float4* src = pc.row(k0 + j0 + j);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[j][i] = __ldg(src + i * 32 + col);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (lk[j] == -CUDART_INF_F) continue;
+        const float w = expf(lk[j] - M);
+        wsum += w;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          acc[i].x = fmaf(w, v[j][i].x, acc[i].x);
+          acc[i].y = fmaf(w, v[j][i].y, acc[i].y);
+          acc[i].z = fmaf(w, v[j][i].z, acc[i].z);
+          acc[i].w = fmaf(w, v[j][i].w, acc[i].w);
+        }
+      }
     }
   }
   const float inv = 1.f / wsum;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kVec; ++i) {
     float4 v = acc[i];
     v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-    reinterpret_cast<float4*>(out_o)[i * 32 + lane] = v;
+    reinterpret_cast<float4*>(out_o)[i * 32 + col] = v;
   }
-  if (lane == 0 && out_lse) *out_lse = M + logf(wsum);
+  if (lane == 0 && out_lse && part == 0) *out_lse = M + logf(wsum);
 }
 
 }  // namespace dcpmla

@@ -6,8 +6,12 @@
 // counts its slice's digits among the keys that match the prefix so far, the
 // histograms are summed over distributed shared memory, and the digit in
 // which the want-th key falls extends the prefix.  The keys above T are taken
-// and, of those equal to T, the first `ties`.  The result is a bit per index
-// in the owning CTA's shared memory, independent of the cluster's size.
+// and, of those equal to T, the first ones.  The result is a bit per index in
+// the owning CTA's shared memory, independent of the cluster's size.
+//
+// What bounds it for all but the longest inputs is the number of barriers, not
+// the keys: a pass has two (counts complete; digit known), one warp scans the
+// 256 bins, and slices of up to kHeld keys a thread stay in registers.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -21,27 +25,39 @@ namespace topk {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kBins = 256;
+constexpr int kHeld = 16;        // keys a thread holds in registers
+constexpr int kMaxCluster = 8;   // the largest portable cluster
+constexpr int kPasses = 4;
 
 struct Ctl {
-  uint32_t hist[2][kBins];    // this CTA's digit counts, by pass parity
-  uint32_t total[kBins];      // the cluster's
+  uint32_t hist[kPasses][kBins];   // this CTA's digit counts
+  uint32_t total[kBins];           // the cluster's, of the current pass
   int warp_sums[kThreads / 32];
-  int digit, above;           // chosen digit and the keys above it
-  int share[2];               // what the other CTAs of the cluster read of this one
+  int digit, above, equal;         // chosen digit, keys above it and in it (whole cluster)
+  int share[2];                    // what the other CTAs of the cluster read of this one
+  int offs[2][kThreads];           // emit(): entries before each word of a batch
 };
 
-// fp32 -> a key in the same order; NaN below everything.
+// fp32 -> a key in the same order; NaN below everything, -0 equal to 0.
 __device__ __forceinline__ uint32_t key_of(float x) {
   if (x != x) return 0u;
-  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);    // -0 equals 0
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
 // The value of a key that is not NaN's.
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
+// Barrier over the cluster (over the block if that is the cluster).
+__device__ __forceinline__ void sync(cg::cluster_group& cl) {
+  if (cl.num_blocks() == 1)
+    __syncthreads();
+  else
+    cl.sync();
 }
 
 // Sum of `share[which]` over the CTAs before this one (call between cluster
@@ -52,60 +68,184 @@ __device__ __forceinline__ int before(cg::cluster_group& cl, Ctl& c, int which) 
   return s;
 }
 
-// Marks the taken indices of this CTA's slice [lo, hi) in `bits` (bit i - lo;
-// room for ceil((hi - lo) / 32) words).  key(i) is called for indices of the
-// slice, several times.  All threads of all CTAs of the cluster call it with
-// the same n and 1 <= want <= n.
-template <class KeyFn>
-__device__ void mark(cg::cluster_group& cl, Ctl& c, int lo, int hi, int want, uint32_t* bits,
-                     KeyFn&& key) {
-  const int tid = threadIdx.x;
+// Adds one to h[d] for every lane with `in`; a warp whose counted lanes agree
+// (keys of like size share their leading digits) adds once.
+__device__ __forceinline__ void count(uint32_t* h, bool in, uint32_t d) {
+  const uint32_t act = __ballot_sync(0xffffffffu, in);
+  if (!act) return;
+  const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(act) - 1);
+  if (__all_sync(0xffffffffu, !in || d == d0)) {
+    if ((threadIdx.x & 31) == 0) atomicAdd(&h[d0], (uint32_t)__popc(act));
+  } else if (in) {
+    atomicAdd(&h[d], 1u);
+  }
+}
+
+// mark() for slices whose keys are read again in every pass (kPer 0), or of at
+// most kPer keys a thread, held in registers.  key(i, first): `first` says that
+// the index is looked at for the first time.
+template <int kPer, class KeyFn>
+__device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo, int hi, int want,
+                                          uint32_t* bits, KeyFn&& key) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  constexpr int kRegs = kPer > 0 ? kPer : 1;
+  uint32_t held[kRegs];
+  if constexpr (kPer > 0) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = lo + j * kThreads + tid;
+      held[j] = i < hi ? key(i, true) : 0u;
+    }
+  }
+  // f(index, key, inside) for this thread's keys, in rounds of kThreads; all
+  // threads take part in every round
+  bool first = true;
+  auto rounds = [&](auto&& f) {
+    if constexpr (kPer > 0) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (lo + j * kThreads < hi) {
+          const int i = lo + j * kThreads + tid;
+          f(i, held[j], i < hi);
+        }
+    } else {
+      for (int base = lo; base < hi; base += 8 * kThreads) {
+        uint32_t k[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = base + j * kThreads + tid;
+          k[j] = i < hi ? key(i, first) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (base + j * kThreads < hi) {
+            const int i = base + j * kThreads + tid;
+            f(i, k[j], i < hi);
+          }
+      }
+      first = false;
+    }
+  };
+  for (int b = tid; b < kPasses * kBins; b += kThreads) (&c.hist[0][0])[b] = 0;
+  __syncthreads();
   uint32_t prefix = 0, mask = 0;
-  int left = want, eq_here = 0;
-  for (int pass = 0; pass < 4; ++pass) {
+  int left = want;
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
     const int shift = 24 - 8 * pass;
-    uint32_t* h = c.hist[pass & 1];
-    if (tid < kBins) h[tid] = 0;
-    __syncthreads();
-    for (int i = lo + tid; i < hi; i += kThreads) {
-      const uint32_t k = key(i);
-      if ((k & mask) == prefix) atomicAdd(&h[(k >> shift) & 255u], 1u);
+    uint32_t* h = c.hist[pass];
+    rounds([&](int, uint32_t k, bool in) {
+      count(h, in && (k & mask) == prefix, (k >> shift) & 255u);
+    });
+    sync(cl);
+    if (cl.num_blocks() > 1) {
+      if (tid < kBins) {
+        uint32_t s = 0;
+#pragma unroll
+        for (unsigned r = 0; r < (unsigned)kMaxCluster; ++r)
+          if (r < cl.num_blocks()) s += cl.map_shared_rank(h, r)[tid];
+        c.total[tid] = s;
+      }
+      __syncthreads();
+      h = c.total;
     }
-    cl.sync();
-    int v = 0;
-    if (tid < kBins) {
-      // bin 255 - tid, so that a running sum goes from the largest digit down
-      for (unsigned r = 0; r < cl.num_blocks(); ++r)
-        v += (int)cl.map_shared_rank(h, r)[kBins - 1 - tid];
-    }
-    int tot;
-    const int ex = block_exclusive_scan(v, c.warp_sums, &tot);
-    if (tid < kBins && ex < left && left <= ex + v) {
-      c.digit = kBins - 1 - tid;
-      c.above = ex;
+    if (tid < 32) {
+      // lane l: bins 255 - 8 l .. 248 - 8 l, from the largest digit down
+      int v[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = (int)h[kBins - 1 - 8 * lane - e];
+        sum += v[e];
+      }
+      int ex = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, ex, o);
+        if (lane >= o) ex += y;
+      }
+      ex -= sum;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (ex < left && left <= ex + v[e]) {
+          c.digit = kBins - 1 - 8 * lane - e;
+          c.above = ex;
+          c.equal = v[e];
+        }
+        ex += v[e];
+      }
     }
     __syncthreads();
     left -= c.above;
     prefix |= (uint32_t)c.digit << shift;
     mask |= 255u << shift;
-    eq_here = (int)h[c.digit];
   }
-  // the last pass's histogram counts the keys equal to T
-  if (tid == 0) c.share[0] = eq_here;
-  cl.sync();
-  int seen = before(cl, c, 0);
-  for (int base = lo; base < hi; base += kThreads) {
-    const int i = base + tid;
-    const uint32_t k = i < hi ? key(i) : 0u;
-    const bool eq = i < hi && k == prefix;
-    int tot;
-    const int rank = seen + block_exclusive_scan(eq ? 1 : 0, c.warp_sums, &tot);
-    seen += tot;
-    const bool take = i < hi && (k > prefix || (eq && rank < left));
+  // The last pass's histogram counts the keys equal to T.  Their order matters
+  // only if some of them are left out.
+  const bool all = left == c.equal;
+  int seen = 0;
+  if (!all) {
+    if (tid == 0) c.share[0] = (int)c.hist[kPasses - 1][c.digit];
+    sync(cl);
+    seen = before(cl, c, 0);
+  }
+  rounds([&](int i, uint32_t k, bool in) {
+    bool take = in && (all ? k >= prefix : k > prefix);
+    if (!all) {
+      const bool eq = in && k == prefix;
+      int tot;
+      const int rank = seen + block_exclusive_scan(eq ? 1 : 0, c.warp_sums, &tot);
+      seen += tot;
+      take = take || (eq && rank < left);
+    }
     const uint32_t word = __ballot_sync(0xffffffffu, take);
-    if ((tid & 31) == 0 && i < hi) bits[(i - lo) >> 5] = word;
+    if (lane == 0 && in) bits[(i - lo) >> 5] = word;
+  });
+  sync(cl);      // `bits` complete; the shared fields may be written again
+}
+
+// Marks the taken indices of this CTA's slice [lo, hi) in `bits` (bit i - lo;
+// room for ceil((hi - lo) / 32) words).  key(i, first) is called for every index
+// of the slice, with `first` once and possibly again without.  All threads of all CTAs of the cluster call
+// it with the same n and 1 <= want <= n.
+template <class KeyFn>
+__device__ __forceinline__ void mark(cg::cluster_group& cl, Ctl& c, int lo, int hi, int want,
+                                     uint32_t* bits, KeyFn&& key) {
+  const int n = hi - lo;
+  if (n <= 2 * kThreads)
+    mark_keys<2>(cl, c, lo, hi, want, bits, key);
+  else if (n <= kHeld * kThreads)
+    mark_keys<kHeld>(cl, c, lo, hi, want, bits, key);
+  else
+    mark_keys<0>(cl, c, lo, hi, want, bits, key);
+}
+
+// Numbers the set bits of kLists masks of the slice in index order:
+// f(list, index, place) for each.  word(list, w) gives the mask of word w;
+// places start at base[list], counted over the CTAs before this one.  totals
+// of the slice come back in base.
+template <int kLists, class WordFn, class F>
+__device__ __forceinline__ void emit(Ctl& c, int lo, int hi, int (&base)[kLists], WordFn&& word,
+                                     F&& f) {
+  const int words = (hi - lo + 31) / 32, lane = threadIdx.x & 31;
+  for (int w0 = 0; w0 < words; w0 += kThreads) {
+    const int w = w0 + threadIdx.x;
+#pragma unroll
+    for (int l = 0; l < kLists; ++l) {
+      int tot;
+      const int ex = block_exclusive_scan(w < words ? __popc(word(l, w)) : 0, c.warp_sums, &tot);
+      c.offs[l][threadIdx.x] = base[l] + ex;
+      base[l] += tot;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x >> 5; k < kThreads && w0 + k < words; k += kThreads / 32)
+#pragma unroll
+      for (int l = 0; l < kLists; ++l) {
+        const uint32_t m = word(l, w0 + k);
+        if ((m >> lane) & 1u)
+          f(l, lo + 32 * (w0 + k) + lane, c.offs[l][k] + __popc(m & ((1u << lane) - 1u)));
+      }
+    __syncthreads();
   }
-  cl.sync();      // `bits` complete; share may be written again
 }
 
 // Slice of CTA `rank` of `size` over n indices, in multiples of 32.
@@ -116,6 +256,21 @@ __device__ __forceinline__ void slice(int n, unsigned rank, unsigned size, int* 
 }
 inline int slice_words(long long n, int size) {
   return (int)(((n + size - 1) / size + 31) / 32);
+}
+
+// CTAs a cluster takes for rows of up to n keys.  A cluster's barriers cost
+// some 3 us over a block's (7 against 10 us at 8 keys, 14 against 17 at 2,112),
+// so one CTA works alone up to 4,096; past that as many as leave 2,048 keys each
+// while the clusters fit the device's waves (clusters of 8 for 64 rows: twice
+// the time of clusters of 4).
+inline int cluster_size(long long n, int rows, int sms) {
+#ifdef FORCE_SIZE
+  return FORCE_SIZE;
+#endif
+  int size = 1;
+  if (n <= 4096) return size;
+  while (size < kMaxCluster && n > 2048ll * size && 2ll * rows * size <= 2ll * sms) size *= 2;
+  return size;
 }
 
 // Launches `kernel` with `rows` clusters of `size` CTAs (grid x = cluster rank).

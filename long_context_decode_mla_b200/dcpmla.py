@@ -358,24 +358,38 @@ def _kv(kv_dtype) -> int:
 
 
 def _nbytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def _expect(name, t, dtype, shape=None):
     """A tensor argument that is passed on as a raw pointer: its type, shape and order."""
     if t is None:
         return
-    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
         want = f"{dtype}" + ("" if shape is None else f" {list(shape)}")
         raise ValueError(f"{name} must be contiguous {want}, got {t.dtype} {list(t.shape)}")
 
 
-def _on_current_device(*tensors):
-    """Raw pointers go to kernels on the current device's stream: nothing else may pass."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+def _here(stream, *tensors) -> int:
+    """The stream to enqueue on (the current one unless given), once every tensor is known to lie on
+    the current device: their raw pointers go to kernels there."""
+    dev = -1
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != cur):
-            raise ValueError(f"a tensor on {t.device} was given to a call on cuda device {cur}")
+        if t is None:
+            continue
+        at = t.get_device()                   # -1: host memory
+        if dev < 0 and at >= 0:
+            dev = torch.cuda.current_device()
+        if at < 0 or at != dev:
+            raise ValueError(f"a tensor on {t.device} was given to a call on cuda device {dev}")
+    if stream is None:
+        # torch.cuda.current_stream() builds an object for 3 us, a third of a small call
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _query_shape(q) -> tuple[int, int, int]:
@@ -392,6 +406,16 @@ def _expect_table(block_table, seq_lens, batch):
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table must be [{batch}, stride], got {list(block_table.shape)}")
     _expect("block_table", block_table, torch.int32)
+
+
+def _expect_cache(kv_cache, kv_dtype, num_blocks, block_size) -> int:
+    """The format's code, for a cache that holds num_blocks blocks in it."""
+    kvd = _kv(kv_dtype)
+    row = 656 if kvd == KV_DTYPES["fp8"] else 1152
+    if not kv_cache.is_contiguous() or kv_cache.nbytes < num_blocks * block_size * row:
+        raise ValueError(f"kv_cache must be contiguous and hold {num_blocks} blocks of {block_size} "
+                         f"rows of {row} bytes, got {kv_cache.dtype} {list(kv_cache.shape)}")
+    return kvd
 
 
 def _size(fn, *args) -> int:
@@ -411,14 +435,15 @@ def mla_block_summary(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_s
     a decode step); ``flags`` an optional one-element int32 device tensor.
     """
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
     _expect_table(block_table, seq_lens, seq_lens.shape[0])
     _expect("first_positions", first_positions, torch.int32, tuple(seq_lens.shape))
     _expect("summaries", summaries, torch.uint8, (nb, SUMMARY_BYTES))
-    _on_current_device(kv_cache, block_table, seq_lens, first_positions, summaries, flags)
+    st = _here(stream, kv_cache, block_table, seq_lens, first_positions, summaries, flags)
     rc = lib().mla_block_summary(
-        _ptr(kv_cache), _kv(kv_dtype), nb, block_size, _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), _ptr(first_positions), block_table.shape[0], shard_id, num_shards,
-        _ptr(summaries), _ptr(flags), _stream(stream))
+        _at(kv_cache), kvd, nb, block_size, _at(block_table), block_table.shape[1],
+        _at(seq_lens), _at(first_positions), block_table.shape[0], shard_id, num_shards,
+        _at(summaries), _at(flags), st)
     _check(rc, "mla_block_summary")
 
 
@@ -444,12 +469,13 @@ def mla_block_select(q, summaries, block_table, seq_lens, shard_id, num_shards, 
         _expect(name, t, torch.int32)
         if t is not None and t.numel() != n:
             raise ValueError(f"{name} must hold {n} values, got {list(t.shape)}")
-    _on_current_device(q, summaries, block_table, seq_lens, out_table, out_lens, out_blocks, workspace)
+    st = _here(stream, q, summaries, block_table, seq_lens, out_table, out_lens, out_blocks,
+               workspace)
     rc = lib().mla_block_select(
-        _ptr(q), _ptr(summaries), summaries.shape[0], block_size, _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
-        sink_blocks, recent_blocks, _ptr(out_blocks), _ptr(out_table), _ptr(out_lens),
-        _ptr(workspace), _nbytes(workspace), _stream(stream))
+        _at(q), _at(summaries), summaries.shape[0], block_size, _at(block_table),
+        block_table.shape[1], _at(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
+        sink_blocks, recent_blocks, _at(out_blocks), _at(out_table), _at(out_lens),
+        _at(workspace), _nbytes(workspace), st)
     _check(rc, "mla_block_select")
 
 
@@ -469,6 +495,7 @@ def mla_decode_blocks(q, kv_cache, kv_dtype, summaries, block_table, seq_lens, s
     include/dcpmla.h): q [B, H, 576] or [B, q_len, H, 576]."""
     B, Q, H = _query_shape(q)
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
     _expect_table(block_table, seq_lens, B)
     _expect("summaries", summaries, torch.uint8, (nb, SUMMARY_BYTES))
     for name, t, dtype, n in (("out_partial", out_partial, torch.float32, B * Q * H * V_DIM),
@@ -478,14 +505,14 @@ def mla_decode_blocks(q, kv_cache, kv_dtype, summaries, block_table, seq_lens, s
         if t is not None and t.numel() != n:
             raise ValueError(f"{name} must hold {n} values, got {list(t.shape)}")
     impl_code = IMPLS[impl] if isinstance(impl, str) else int(impl)
-    _on_current_device(q, kv_cache, summaries, block_table, seq_lens, out_partial, out_lse, out_blocks,
-                       workspace)
+    st = _here(stream, q, kv_cache, summaries, block_table, seq_lens, out_partial, out_lse,
+               out_blocks, workspace)
     rc = lib().mla_decode_blocks(
-        _ptr(q), _ptr(kv_cache), _kv(kv_dtype), _ptr(summaries), nb, block_size, _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
-        sink_blocks, recent_blocks, float(softmax_scale), _ptr(out_partial), _ptr(out_lse),
-        _ptr(out_blocks), _ptr(workspace), _nbytes(workspace), num_splits, impl_code,
-        _stream(stream))
+        _at(q), _at(kv_cache), kvd, _at(summaries), nb, block_size, _at(block_table),
+        block_table.shape[1], _at(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
+        sink_blocks, recent_blocks, float(softmax_scale), _at(out_partial), _at(out_lse),
+        _at(out_blocks), _at(workspace), _nbytes(workspace), num_splits, impl_code,
+        st)
     _check(rc, "mla_decode_blocks")
 
 
@@ -502,17 +529,18 @@ def mla_attention_mass(q, kv_cache, kv_dtype, block_table, seq_lens, shard_id, n
     LSE of the same queries and heads."""
     B, Q, H = _query_shape(q)
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
     _expect_table(block_table, seq_lens, B)
     _expect("lse", lse, torch.float32)
     if lse.numel() != B * Q * H:
         raise ValueError(f"lse must hold {B * Q * H} values, got {list(lse.shape)}")
     _expect("mass", mass, torch.float32, (B, mass.shape[-1]))
-    _on_current_device(q, kv_cache, block_table, seq_lens, lse, mass, workspace)
+    st = _here(stream, q, kv_cache, block_table, seq_lens, lse, mass, workspace)
     rc = lib().mla_attention_mass(
-        _ptr(q), _ptr(kv_cache), _kv(kv_dtype), nb, block_size, _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), B, H, Q, shard_id, num_shards, float(softmax_scale),
-        _ptr(lse), float(decay), _ptr(mass), mass.shape[-1], _ptr(workspace), _nbytes(workspace),
-        num_splits, _stream(stream))
+        _at(q), _at(kv_cache), kvd, nb, block_size, _at(block_table),
+        block_table.shape[1], _at(seq_lens), B, H, Q, shard_id, num_shards, float(softmax_scale),
+        _at(lse), float(decay), _at(mass), mass.shape[-1], _at(workspace), _nbytes(workspace),
+        num_splits, st)
     _check(rc, "mla_attention_mass")
 
 
@@ -529,6 +557,7 @@ def mla_cache_evict(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_sha
     are [B, rows]; an output may be the input itself."""
     B = seq_lens.shape[0]
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
+    kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
     _expect_table(block_table, seq_lens, B)
     shape = (B, mass.shape[-1])
     for name, t, dtype, sh in (("mass", mass, torch.float32, shape),
@@ -538,13 +567,13 @@ def mla_cache_evict(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_sha
                                ("rows", rows, torch.int32, (B,)),
                                ("rows_out", rows_out, torch.int32, (B,))):
         _expect(name, t, dtype, sh)
-    _on_current_device(kv_cache, block_table, seq_lens, rows, mass, positions, mass_out, positions_out,
-                       rows_out, workspace)
+    st = _here(stream, kv_cache, block_table, seq_lens, rows, mass, positions, mass_out,
+               positions_out, rows_out, workspace)
     rc = lib().mla_cache_evict(
-        _ptr(kv_cache), _kv(kv_dtype), nb, block_size, _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), _ptr(rows), B, shard_id, num_shards, _ptr(mass), _ptr(positions),
-        mass.shape[-1], budget, sink, recent, _ptr(mass_out), _ptr(positions_out), _ptr(rows_out),
-        _ptr(workspace), _nbytes(workspace), _stream(stream))
+        _at(kv_cache), kvd, nb, block_size, _at(block_table), block_table.shape[1],
+        _at(seq_lens), _at(rows), B, shard_id, num_shards, _at(mass), _at(positions),
+        mass.shape[-1], budget, sink, recent, _at(mass_out), _at(positions_out), _at(rows_out),
+        _at(workspace), _nbytes(workspace), st)
     _check(rc, "mla_cache_evict")
 
 
@@ -659,7 +688,8 @@ class DcpDecoder:
                  recent_blocks=1):
         self.batch, self.heads, self.num_shards = batch, heads, num_shards
         self.num_splits, self.impl, self.topk, self.q_len = num_splits, impl, topk, q_len
-        self.block_topk, self.sink_blocks, self.recent_blocks = block_topk, sink_blocks, recent_blocks
+        self.block_topk = block_topk
+        self.sink_blocks, self.recent_blocks = sink_blocks, recent_blocks
         rows = heads * q_len                 # multi-query: rows [q_len][heads]
         dev = torch.device(device)
         self.partials = torch.empty(num_shards, batch, rows, V_DIM, device=dev)

@@ -110,6 +110,8 @@ def test_the_binding_checks_what_it_passes_on():
                 good[fn](**{name: bad[name]})
         with pytest.raises(ValueError, match="cuda device"):      # host memory goes to no kernel
             good[fn]()
+    with pytest.raises(ValueError, match="must"):                   # a cache of fewer blocks than it is said to have
+        dcpmla.mla_block_summary(kv, "bf16", t, n, 0, 1, S)
     with pytest.raises(ValueError, match="max_blocks"):
         dcpmla.DcpDecoder(2, 8, 1, block_topk=4, device="cpu")
 
