@@ -745,9 +745,9 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
   rc = run_select(p, sel, static_cast<cudaStream_t>(stream));
   if (rc != DCPMLA_OK) return rc;
   // the chosen blocks of a query are one request of one shard, in a table of their own
-  return mla_decode_partial(q, kv_cache, kv_dtype, num_blocks, block_size, p.out_table, block_topk,
-                            p.out_lens, rows, num_heads, 0, 1, nullptr, 0, softmax_scale,
-                            out_partial, out_lse, workspace, dec, num_splits, impl, stream);
+  return decode_chosen_blocks(q, kv_cache, kv_dtype, num_blocks, p.out_table, block_topk,
+                              p.out_lens, rows, num_heads, softmax_scale, out_partial, out_lse,
+                              workspace, dec, num_splits, impl, stream);
 }
 
 }  // extern "C"

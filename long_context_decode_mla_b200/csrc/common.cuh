@@ -73,6 +73,7 @@ struct PartialParams {
                               // [b * row_stride + 64 k, + 64) of the list
   int row_stride;
   int request_aligned;        // 1: CTA c takes requests [c B / G, (c+1) B / G) whole (no splits)
+  int round_p;                // e4m3 kernel: P's hi term rounded instead of cut (half the error)
   int test_withhold;          // test only: converters skip their first arrival (timeout path)
 };
 

@@ -144,7 +144,7 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
                    int num_shards, const int32_t* sparse_idx, int topk, float softmax_scale,
                    float* out_partial, float* out_lse, void* workspace, size_t workspace_bytes,
                    int num_splits, int impl, void* stream, int rows_q, int rows_o,
-                   int len_delta, bool identity_table = false) {
+                   int len_delta, bool identity_table = false, bool round_p = false) {
   // ---- scalar checks (fail closed, nothing launched on error) ----
   const bool withhold = (impl & DCPMLA_TEST_WITHHOLD_ARRIVAL) != 0;
   impl &= ~DCPMLA_TEST_WITHHOLD_ARRIVAL;
@@ -202,6 +202,7 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
   p.ws_lse = reinterpret_cast<float*>(ws + ws_lse_offset(slots, num_heads));
   p.ws_list = list_ints ? reinterpret_cast<int*>(ws + ws_list_offset(slots, num_heads)) : nullptr;
   p.num_ctas = ctas;
+  p.round_p = round_p ? 1 : 0;
   p.test_withhold = withhold ? 1 : 0;
   p.q_image = ws + ws_total((long long)ctas + batch, num_heads);
 
@@ -290,6 +291,17 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
 }
 
 }  // namespace
+
+int dcpmla::decode_chosen_blocks(const void* q, const void* kv_cache, int kv_dtype,
+                                 int64_t num_blocks, const int32_t* table, int stride,
+                                 const int32_t* lens, int rows, int num_heads, float softmax_scale,
+                                 float* out, float* out_lse, void* workspace,
+                                 size_t workspace_bytes, int num_splits, int impl, void* stream) {
+  return decode_partial(q, kv_cache, kv_dtype, num_blocks, kBlock, table, stride, lens, rows,
+                        num_heads, 1, 0, 1, nullptr, 0, softmax_scale, out, out_lse, workspace,
+                        workspace_bytes, num_splits, impl, stream, num_heads, num_heads, 0, false,
+                        true);
+}
 
 extern "C" {
 

@@ -26,6 +26,14 @@ bool f8_supports(const PartialParams& p, int kv_dtype);
 cudaError_t launch_split_combine(const PartialParams& p, cudaStream_t st);
 cudaError_t launch_dcp_merge(const float* partials, const float* lses, int num_shards, int batch,
                              int heads, float* out, float* out_lse, cudaStream_t st);
+// mla_decode_partial over `rows` requests of one shard, each its own table of
+// chosen blocks, with P rounded (PartialParams::round_p): the few thousand rows
+// of a choice average less of P's rounding away than a long dense context.
+int decode_chosen_blocks(const void* q, const void* kv_cache, int kv_dtype, int64_t num_blocks,
+                         const int32_t* table, int stride, const int32_t* lens, int rows,
+                         int num_heads, float softmax_scale, float* out, float* out_lse,
+                         void* workspace, size_t workspace_bytes, int num_splits, int impl,
+                         void* stream);
 int simt_sparse_chunk_max();
 cudaError_t launch_sparse_gather(const PartialParams& p, int row_bytes, int maxblk,
                                  uint8_t* gathered, int* counts, cudaStream_t st);

@@ -234,11 +234,15 @@ __device__ __forceinline__ uint16_t f16_sat(float x) {
 // and lo terms, four bytes each (first token in the low byte).  hi keeps the
 // sign, exponent and 3 leading mantissa bits of each fp16 value (4
 // significant bits, exact in e4m3 in its normal range); lo = x - hi is exact
-// in fp16 and below 2^-3 |x|, and its encoding rounds it to 4 bits.
+// in fp16 and below 2^-3 |x|, and its encoding rounds it to 4 bits.  With
+// kRound hi is rounded to those bits instead of cut (half a step added first:
+// x >= 0, so no carry leaves a half-word), lo is at most 2^-4 |x| of either
+// sign, and the two together are half as far from x.
+template <bool kRound>
 __device__ __forceinline__ void split_hilo4(uint32_t x0, uint32_t x1, uint32_t& hi,
                                             uint32_t& lo) {
-  constexpr uint32_t kLead = 0xFF80FF80u;
-  const uint32_t h0 = x0 & kLead, h1 = x1 & kLead;
+  constexpr uint32_t kLead = 0xFF80FF80u, kStep = kRound ? 0x00400040u : 0u;
+  const uint32_t h0 = (x0 + kStep) & kLead, h1 = (x1 + kStep) & kLead;
   const uint32_t l0 = hsub2_rn(x0, h0), l1 = hsub2_rn(x1, h1);
   asm("{\n .reg .b16 a, b;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n"
@@ -649,6 +653,7 @@ __device__ __forceinline__ void staging_role(const PartialParams& p, F8Ctl& c, u
 // threads; a barrier-wide vote tells whether any thread's tile maximum
 // exceeds the max in use by more than 2^3, and only then are the maxima
 // exchanged through shared memory.
+template <bool kRound>
 __device__ __forceinline__ void softmax_role(const PartialParams& p, F8Ctl& c, uint8_t* base, int nseg,
                              uint32_t& tau, uint32_t& sigma, uint32_t& pi) {
   const int T = threadIdx.x;                 // 0..255
@@ -827,7 +832,7 @@ __device__ __forceinline__ void softmax_role(const PartialParams& p, F8Ctl& c, u
       uint32_t hw[4], lw[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        split_hilo4(hmul2_rn(pp[2 * j], swv[2 * j]), hmul2_rn(pp[2 * j + 1], swv[2 * j + 1]),
+        split_hilo4<kRound>(hmul2_rn(pp[2 * j], swv[2 * j]), hmul2_rn(pp[2 * j + 1], swv[2 * j + 1]),
                     hw[j], lw[j]);
       *reinterpret_cast<uint4*>(pbuf + (2 * g) * kPVar + sw64(h, unit)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
       *reinterpret_cast<uint4*>(pbuf + (2 * g + 1) * kPVar + sw64(h, unit)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
@@ -904,7 +909,7 @@ __device__ __forceinline__ void block_bar() { ptx::named_bar(kBarBlock, kThreads
 // The batch loop of one side of the register split: kSoft runs the softmax
 // warps, !kSoft every other role and, at the end, the drains of the
 // asynchronous arrivals.  Both sides take the same block barriers.
-template <bool kSoft, bool kListed>
+template <bool kSoft, bool kListed, bool kRound>
 __device__ __forceinline__ void run_roles(const F8Params& P, const PartialParams& p, F8Ctl& c,
                                           uint8_t* base, int lo, int hi) {
   const int warp = threadIdx.x >> 5;
@@ -917,7 +922,7 @@ __device__ __forceinline__ void run_roles(const F8Params& P, const PartialParams
     const int nseg = min(kMaxSegF8, total - first);
     if (nseg <= 0) break;
     if constexpr (kSoft) {
-      softmax_role(p, c, base, nseg, tau, sigma, pi);
+      softmax_role<kRound>(p, c, base, nseg, tau, sigma, pi);
     } else {
       if (warp == kProdWarp) {
         producer_role<kListed>(P, p, c, base, nseg, tau, fills);
@@ -976,7 +981,7 @@ __device__ __forceinline__ void run_roles(const F8Params& P, const PartialParams
   }
 }
 
-template <bool kListed>
+template <bool kListed, bool kRound>
 __global__ void __launch_bounds__(kThreads, 1) partial_f8_kernel(const __grid_constant__ F8Params P) {
   // dense only: a known-null index list lets the compiler drop the sparse
   // branches of the shared schedule
@@ -1044,10 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 1) partial_f8_kernel(const __grid_co
   // end so that each is compiled within its own budget.
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    run_roles<true, kListed>(P, p, c, base, lo, hi);
+    run_roles<true, kListed, kRound>(P, p, c, base, lo, hi);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    run_roles<false, kListed>(P, p, c, base, lo, hi);
+    run_roles<false, kListed, kRound>(P, p, c, base, lo, hi);
   }
   if (c.abort && threadIdx.x == 0 && p.flags) atomicOr(p.flags, kFlagTimeout);
   ptx::tc_fence_before();
@@ -1101,7 +1106,7 @@ bool encode_maps(const PartialParams& p, CUtensorMap* rows, CUtensorMap* scales)
 }
 
 std::mutex g_attr_mutex;
-bool g_attr_done[2][kMaxDevicesConfigured] = {};   // [listed rows][device]
+bool g_attr_done[3][kMaxDevicesConfigured] = {};   // [dense, listed rows, rounded P][device]
 
 }  // namespace
 
@@ -1140,13 +1145,16 @@ cudaError_t launch_partial_f8(const PartialParams& p, cudaStream_t st) {
   if (dev < 0 || dev >= kMaxDevicesConfigured) return cudaErrorInvalidDevice;
   const int smem = (int)kSmemBytes;
   const bool listed = p.row_ids != nullptr;
-  auto kernel = listed ? partial_f8_kernel<true> : partial_f8_kernel<false>;
+  const int form = listed ? 1 : p.round_p ? 2 : 0;
+  auto kernel = listed      ? partial_f8_kernel<true, false>
+                : p.round_p ? partial_f8_kernel<false, true>
+                            : partial_f8_kernel<false, false>;
   {
     // raise the shared-memory limit once per device and instantiation, so
     // that later launches (including ones captured into a CUDA graph) are
     // plain launches
     std::lock_guard<std::mutex> lock(g_attr_mutex);
-    if (!g_attr_done[listed][dev]) {
+    if (!g_attr_done[form][dev]) {
       // the in-kernel register split assumes exactly kLaunchRegs registers
       // per thread at launch; with fewer, the softmax warpgroups' increase
       // could never be granted
@@ -1157,7 +1165,7 @@ cudaError_t launch_partial_f8(const PartialParams& p, cudaStream_t st) {
         return cudaErrorInvalidDeviceFunction;
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
-      g_attr_done[listed][dev] = true;
+      g_attr_done[form][dev] = true;
     }
   }
   if (!p.q_image_ready) {
