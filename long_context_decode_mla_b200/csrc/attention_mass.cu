@@ -227,6 +227,7 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
         const uint32_t dq = ptx::smem_addr(base);
         ptx::mbar_arrive_expect_tx(&c.q_full, kQBytes);
         if constexpr (kDtype == kKvFp8) {
+          ptx::wait_primary();       // the images' kernel
           ptx::bulk_g2s(dq, p.q_image + (size_t)cur.v.b * kQImageBytes, kQBytes, &c.q_full);
         } else {
 #pragma unroll 1
@@ -345,9 +346,11 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
         float2 f = make_float2(0.f, INFINITY);     // rows past the pass weigh nothing
         if (h < p.heads) {
           f.x = sl2;
-          if constexpr (kDtype == kKvFp8)
-            f.x *= __ldg(reinterpret_cast<const float*>(p.q_image + (size_t)b * kQImageBytes +
-                                                        kQBytes) + h);
+          if constexpr (kDtype == kKvFp8) {
+            ptx::wait_primary();
+            f.x *= __ldcg(reinterpret_cast<const float*>(p.q_image + (size_t)b * kQImageBytes +
+                                                         kQBytes) + h);
+          }
           const float l = __ldg(m.lse + (size_t)b * p.rows_o + h);
           f.y = l == -INFINITY ? INFINITY : l * kLog2e;
         }
@@ -483,6 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     first += kMaxSeg;
     if (total <= first) break;
   }
+  // a CTA without tiles waits too: this kernel's end implies the images' kernel's
+  ptx::wait_primary();
   // Drain: every asynchronous arrival lands before the CTA exits (after a
   // timeout these waits are bounded too).
   if ((threadIdx.x & 31) == 0 && warp >= kMmaWarp && warp < kMmaWarp + S::kIssuers) {
@@ -546,8 +551,8 @@ cudaError_t launch_mass(MassParams& m, int dev, cudaStream_t st) {
     const cudaError_t e = launch_q_image(p, st);
     if (e != cudaSuccess) return e;
   }
-  mass_kernel<kDtype><<<p.num_ctas, kThreads, smem, st>>>(m);
-  return cudaGetLastError();
+  return launch_kernel(mass_kernel<kDtype>, dim3(p.num_ctas), kThreads, smem, st, 0,
+                       kDtype == kKvFp8, m);
 }
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }

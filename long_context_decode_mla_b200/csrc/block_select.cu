@@ -50,6 +50,7 @@ struct SelectParams {
   int topk, sink, recent;
   int tiles;                   // scoring tiles per row (from the table's stride)
   uint8_t* q_codes;            // [rows][kQBytes]
+  uint8_t* q_image;            // the e4m3 decode kernel's Q images, or nullptr
   int num_ctas;                // SMs
   float* scores;               // [rows][tiles][heads][kTile]
   uint32_t* tile_max;          // [rows][tiles][heads], as ordered keys
@@ -77,21 +78,41 @@ __device__ __forceinline__ int rows_of(const SelectParams& p, int r, int* blocks
   return n;
 }
 
-// Query image of one row: a warp per group of head blockIdx.y.
-__global__ void __launch_bounds__(160) q_codes_kernel(const SelectParams p) {
-  const int r = blockIdx.x, h = blockIdx.y, g = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Query images of two heads of one row: a warp per head and scale group, four
+// values a lane (the IEEE divisions are what it spends its time on: 72 of them a
+// thread took 9 us).  With an e4m3 cache the decode kernel's Q image (its layout
+// and rules: q_image.cuh) is built from the same loads.
+constexpr int kCodeThreads = 2 * kGroups * 32;
+__global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParams p) {
+  ptx::launch_dependents();
+  __shared__ uint32_t top[2][4];        // latent: largest |q| bits of each group
+  const int r = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp / kGroups, g = warp % kGroups, h = blockIdx.y * 2 + half;
   const bool live = h < p.heads;
-  const __nv_bfloat16* q = p.q + ((size_t)r * p.heads + (live ? h : 0)) * kHeadDim;
-  const int v = g < 4 ? 4 : 2, d = v * lane;
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
-  float amax = 0.f;
-  for (int e = 0; e < v; ++e) {
-    x[e] = live ? __bfloat162float(q[128 * g + d + e]) : 0.f;
-    if (!(fabsf(x[e]) <= 3.4028234663852886e38f)) x[e] = 0.f;
-    amax = fmaxf(amax, fabsf(x[e]));
+  const __nv_bfloat16* q =
+      p.q + ((size_t)r * p.heads + (live ? h : 0)) * kHeadDim + 128 * g;
+  const int d = (g < 4 ? 4 : 2) * lane;
+  uint2 w = make_uint2(0, 0);
+  if (live) {
+    if (g < 4)
+      w = __ldg(reinterpret_cast<const uint2*>(q + d));
+    else
+      w.x = __ldg(reinterpret_cast<const uint32_t*>(q + d));
   }
+  float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+  uint32_t finite = 0, any = 0;         // largest magnitudes, as bits: finite ones, all but NaN
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t m = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+    if (m <= 0x7F800000u) any = max(any, m);
+    if (m < 0x7F800000u)
+      finite = max(finite, m);
+    else
+      x[e] = 0.f;
+  }
+  finite = __reduce_max_sync(0xffffffffu, finite);
+  const float amax = __uint_as_float(finite);
   const float step = amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
   uint32_t code = 0;
 #pragma unroll
@@ -100,12 +121,29 @@ __global__ void __launch_bounds__(160) q_codes_kernel(const SelectParams p) {
     code |= ((uint32_t)c & 0xFFu) << (8 * e);
   }
   uint8_t* out = p.q_codes + (size_t)r * kQBytes;
-  uint8_t* at = out + g * kChunk + qimg::sw128(h, d >> 4) + (d & 15);
+  const uint32_t at = g * kChunk + qimg::sw128(h, d >> 4) + (d & 15);
   if (g < 4)
-    *reinterpret_cast<uint32_t*>(at) = code;
+    *reinterpret_cast<uint32_t*>(out + at) = code;
   else
-    *reinterpret_cast<uint16_t*>(at) = (uint16_t)code;
+    *reinterpret_cast<uint16_t*>(out + at) = (uint16_t)code;
   if (lane == 0) reinterpret_cast<float*>(out + kQCodes)[h * 8 + g] = step;
+  if (!p.q_image) return;
+  any = __reduce_max_sync(0xffffffffu, any);
+  if (lane == 0 && g < 4) top[half][g] = any;
+  __syncthreads();
+  uint8_t* img = p.q_image + (size_t)r * kQImageBytes;
+  if (g == 4) {
+    *reinterpret_cast<uint32_t*>(img + qimg::kRope + qimg::sw128(h, d >> 3) + 2 * (d & 7)) = w.x;
+    return;
+  }
+  const uint32_t m = max(max(top[half][0], top[half][1]), max(top[half][2], top[half][3]));
+  const int a = m > 0 ? min(120, max(-120, 7 - ((int)(m >> 23) - 127))) : 0;
+  uint32_t hi, lo;
+  qimg::split_q4(w.x, w.y, __uint_as_float((uint32_t)(127 + a) << 23), hi, lo);
+  *reinterpret_cast<uint32_t*>(img + qimg::kHi + at) = hi;
+  *reinterpret_cast<uint32_t*>(img + qimg::kLo + at) = lo;
+  if (lane == 0 && g == 0)
+    reinterpret_cast<float*>(img + qimg::kFrame)[h] = __uint_as_float((uint32_t)(127 - a) << 23);
 }
 
 // ----------------------------------------------------------- scoring ----
@@ -245,6 +283,7 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
     if (fresh) {
       if (t == 0) {
         if (sigma > 0 && !ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort)) return;
+        ptx::wait_primary();       // the query images' kernel
         // the scorers read the old steps through the generic proxy
         ptx::fence_proxy_async();
         ptx::mbar_arrive_expect_tx(&c.q_full, kQBytes);
@@ -383,6 +422,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
                                              ~static_cast<uintptr_t>(1023));
   ScoreCtl& c = *reinterpret_cast<ScoreCtl*>(base + kOffCtl);
   const int warp = threadIdx.x >> 5;
+  ptx::launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kScoreStages; ++s) {
       ptx::mbar_init(&c.full[s], kCopyThreads);
@@ -410,7 +450,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
       const int i = i0 + threadIdx.x;
       int nb = 0;
       if (i < kRowChunk && r0 + i < rows) rows_of(p, r0 + i, &nb);
-      const int nt = (nb + kTile - 1) / kTile;
+      const int nt = nb > p.topk ? (nb + kTile - 1) / kTile : 0;    // else all are taken
       int tot;
       const int ex = block_exclusive_scan(nt, c.warp_sums, &tot);
       if (i < kRowChunk) {
@@ -432,6 +472,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
     __syncthreads();
     if (c.abort) break;
   }
+  // a CTA without tiles waits too: this kernel's end implies the previous one's
+  ptx::wait_primary();
   // Drain: every asynchronous arrival and copy lands before the CTA exits.
   if (threadIdx.x == kMmaWarp * 32) {
     for (uint32_t s = 0; s < (uint32_t)kScoreStages; ++s) {
@@ -471,6 +513,7 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   int lo, hi;
   topk::slice(nb, cl.block_rank(), cl.num_blocks(), &lo, &hi);
   const int want = min(nb, p.topk);
+  ptx::wait_primary();
   const int tiles = (nb + kTile - 1) / kTile;
   if (threadIdx.x < 64) kmax[threadIdx.x] = 0;
   __syncthreads();
@@ -478,9 +521,9 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
     const uint32_t* tm = p.tile_max + (size_t)r * p.tiles * p.heads;
     const int h = threadIdx.x & 63, t0 = threadIdx.x >> 6;
     uint32_t m = 0;
-    if (h < p.heads) {
+    if (h < p.heads && nb > p.topk) {
 #pragma unroll 4
-      for (int t = t0; t < tiles; t += topk::kThreads / 64) m = max(m, __ldg(tm + t * p.heads + h));
+      for (int t = t0; t < tiles; t += topk::kThreads / 64) m = max(m, __ldcg(tm + t * p.heads + h));
       atomicMax(&kmax[h], m);
     }
   }
@@ -489,7 +532,7 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   __syncthreads();
   for (int k = lo + threadIdx.x; k < hi; k += topk::kThreads) {
     uint32_t key = 0xFFFFFFFFu;
-    if (k >= p.sink && k < nb - p.recent) {
+    if (nb > p.topk && k >= p.sink && k < nb - p.recent) {
       const float* s = p.scores + ((size_t)r * p.tiles + k / kTile) * p.heads * kTile + k % kTile;
       float rank = -INFINITY;
       auto add = [&](float v, int h) {
@@ -500,11 +543,11 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
       for (; h + 16 <= p.heads; h += 16) {
         float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __ldg(s + (h + e) * kTile);
+        for (int e = 0; e < 16; ++e) v[e] = __ldcg(s + (h + e) * kTile);
 #pragma unroll
         for (int e = 0; e < 16; ++e) add(v[e], h + e);
       }
-      for (; h < p.heads; ++h) add(__ldg(s + h * kTile), h);
+      for (; h < p.heads; ++h) add(__ldcg(s + h * kTile), h);
       key = topk::key_of(rank);
     }
     keys[k - lo] = key;
@@ -525,7 +568,9 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   }
   topk::emit<1>(c, lo, hi, pos, [&](int, int w) { return bits[w]; }, [&](int, int k, int at) {
     if (p.out_blocks) p.out_blocks[(size_t)r * p.topk + at] = k;
-    p.out_table[(size_t)r * p.topk + at] = __ldg(p.block_table + (size_t)b * p.bt_stride + k);
+    const int blk = __ldg(p.block_table + (size_t)b * p.bt_stride + k);
+    if ((blk < 0 || (long long)blk >= p.num_blocks) && p.flags) atomicOr(p.flags, kFlagBadBlock);
+    p.out_table[(size_t)r * p.topk + at] = blk;
   });
   if (cl.block_rank() == 0) {
     for (int i = want + threadIdx.x; i < p.topk; i += topk::kThreads) {
@@ -627,12 +672,17 @@ int check_select(const SelectArgs& a, SelectParams* p) {
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   const int rows = p.batch * p.q_len;
-  q_codes_kernel<<<dim3(rows, 64), 160, 0, st>>>(p);
-  score_kernel<<<(int)std::min<long long>(p.num_ctas, (long long)rows * p.tiles), kScoreThreads, kScoreSmem, st>>>(p);
+  q_codes_kernel<<<dim3(rows, 32), kCodeThreads, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(score_kernel, dim3((unsigned)std::min<long long>(p.num_ctas, (long long)rows * p.tiles)),
+                    kScoreThreads, kScoreSmem, st, 0, true, p);
+  if (e != cudaSuccess) return e;
   int size = topk::cluster_size(p.bt_stride, rows, p.num_ctas);
   while ((long long)size * kMaxKeys < p.bt_stride) size *= 2;      // keys and bits in shared memory
   const int words = topk::slice_words(p.bt_stride, size);
-  return topk::launch(choose_kernel, rows, size, (size_t)words * 33 * 4, st, p, words);
+  return launch_kernel(choose_kernel, dim3(size, rows), topk::kThreads, (size_t)words * 33 * 4, st,
+                       size, true, p, words);
 }
 
 // The choice on a workspace part `ws` (laid out by layout()).
@@ -742,6 +792,7 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
   p.out_table = reinterpret_cast<int*>(sel + layout(rows, num_heads, block_table_stride).total);
   p.out_lens = p.out_table + round256((size_t)rows * block_topk * 4) / 4;
   p.flags = static_cast<int*>(workspace);
+  p.q_image = decode_chosen_q_image(kv_dtype, rows, num_heads, num_splits, impl, workspace);
   rc = run_select(p, sel, static_cast<cudaStream_t>(stream));
   if (rc != DCPMLA_OK) return rc;
   // the chosen blocks of a query are one request of one shard, in a table of their own

@@ -144,7 +144,7 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
                    int num_shards, const int32_t* sparse_idx, int topk, float softmax_scale,
                    float* out_partial, float* out_lse, void* workspace, size_t workspace_bytes,
                    int num_splits, int impl, void* stream, int rows_q, int rows_o,
-                   int len_delta, bool identity_table = false, bool round_p = false) {
+                   int len_delta, bool identity_table = false, bool chosen = false) {
   // ---- scalar checks (fail closed, nothing launched on error) ----
   const bool withhold = (impl & DCPMLA_TEST_WITHHOLD_ARRIVAL) != 0;
   impl &= ~DCPMLA_TEST_WITHHOLD_ARRIVAL;
@@ -202,7 +202,9 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
   p.ws_lse = reinterpret_cast<float*>(ws + ws_lse_offset(slots, num_heads));
   p.ws_list = list_ints ? reinterpret_cast<int*>(ws + ws_list_offset(slots, num_heads)) : nullptr;
   p.num_ctas = ctas;
-  p.round_p = round_p ? 1 : 0;
+  // chosen blocks: P rounded, and the caller built the Q images
+  p.round_p = chosen ? 1 : 0;
+  p.q_image_ready = chosen ? 1 : 0;
   p.test_withhold = withhold ? 1 : 0;
   p.q_image = ws + ws_total((long long)ctas + batch, num_heads);
 
@@ -301,6 +303,18 @@ int dcpmla::decode_chosen_blocks(const void* q, const void* kv_cache, int kv_dty
                         num_heads, 1, 0, 1, nullptr, 0, softmax_scale, out, out_lse, workspace,
                         workspace_bytes, num_splits, impl, stream, num_heads, num_heads, 0, false,
                         true);
+}
+
+uint8_t* dcpmla::decode_chosen_q_image(int kv_dtype, int rows, int num_heads, int num_splits,
+                                       int impl, void* workspace) {
+  PartialParams p{};
+  p.q_len = 1;
+  p.heads = num_heads;
+  int ctas = 0;
+  if ((impl != DCPMLA_IMPL_AUTO && impl != DCPMLA_IMPL_TC) || !f8_supports(p, kv_dtype) ||
+      resolve_ctas(num_splits, &ctas) != DCPMLA_OK)
+    return nullptr;
+  return static_cast<uint8_t*>(workspace) + ws_total((long long)ctas + rows, num_heads);
 }
 
 extern "C" {

@@ -22,6 +22,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "select_topk.cuh"
+#include "tc_ptx.cuh"
 
 namespace dcpmla {
 namespace {
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(topk::kThreads) pick_kernel(const EvictParams 
   extern __shared__ __align__(16) uint32_t bits[];
   __shared__ topk::Ctl c;
   topk::cg::cluster_group cl = topk::cg::this_cluster();
+  ptx::launch_dependents();
   const int b = blockIdx.y;
   int L;
   const int n = rows_of(p, b, &L);
@@ -159,12 +161,13 @@ template <int kRowBytes>
 __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictParams p) {
   constexpr int kUnits = kRowBytes / 16, kPer = (kUnits + 7) / 8;
   const int b = blockIdx.y, sub = (threadIdx.x & 31) >> 3, l = threadIdx.x & 7;
-  const int n = __ldg(p.count + b);
+  ptx::wait_primary();
+  const int n = __ldcg(p.count + b);
   const size_t base = (size_t)b * p.mass_stride;
   const int stride = gridDim.x * kMoveWarps * kMoveRows;
   for (int i = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * kMoveRows + sub; i < n; i += stride) {
-    const int src = __ldg(p.movers + (size_t)b * p.budget + i);
-    const int dst = __ldg(p.holes + (size_t)b * p.budget + i);
+    const int src = __ldcg(p.movers + (size_t)b * p.budget + i);
+    const int dst = __ldcg(p.holes + (size_t)b * p.budget + i);
     const uint4* s = reinterpret_cast<const uint4*>(row_at<kRowBytes>(p, b, src));
     uint4* d = reinterpret_cast<uint4*>(row_at<kRowBytes>(p, b, dst));
     if (l == 0) {
@@ -269,16 +272,17 @@ int mla_cache_evict(void* kv_cache, int kv_dtype, int64_t num_blocks, int block_
   int size = topk::cluster_size(most, batch, sms);
   while ((most + size - 1) / size > kMaxRows / topk::kMaxCluster) size *= 2;   // bits in shared memory
   const size_t smem = (size_t)topk::slice_words(most, size) * 4;
-  if (topk::launch(pick_kernel, batch, size, smem, st, p) != cudaSuccess) return DCPMLA_ERR_CUDA;
+  if (launch_kernel(pick_kernel, dim3(size, batch), topk::kThreads, smem, st, size, false, p) !=
+      cudaSuccess)
+    return DCPMLA_ERR_CUDA;
   const int most_moves = (int)std::min<long long>(budget, std::max<long long>(most - budget, 0));
   if (most_moves > 0) {
     constexpr int kCtaRows = kMoveWarps * kMoveRows;
     const int gx = std::max(1, std::min((most_moves + kCtaRows - 1) / kCtaRows, sms * 8 / batch));
     const dim3 grid(gx, batch);
-    if (kv_dtype == DCPMLA_KV_BF16)
-      move_kernel<kRowBytesBf16><<<grid, 32 * kMoveWarps, 0, st>>>(p);
-    else
-      move_kernel<kRowBytesFp8><<<grid, 32 * kMoveWarps, 0, st>>>(p);
+    auto move = kv_dtype == DCPMLA_KV_BF16 ? move_kernel<kRowBytesBf16> : move_kernel<kRowBytesFp8>;
+    if (launch_kernel(move, grid, 32 * kMoveWarps, 0, st, 0, true, p) != cudaSuccess)
+      return DCPMLA_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? DCPMLA_OK : DCPMLA_ERR_CUDA;
 }

@@ -8,6 +8,36 @@
 
 namespace dcpmla {
 
+// Launch with an optional cluster size (0: none) along x; `dependent`: the kernel
+// may start before the stream's previous one is complete and waits for it itself
+// (griddepcontrol).
+template <class... KArgs, class... Args>
+cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t st, int cluster, bool dependent, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 0) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = 1;
+    at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // cuTensorMapEncodeTiled of the driver, nullptr if it has none.
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -34,6 +64,11 @@ int decode_chosen_blocks(const void* q, const void* kv_cache, int kv_dtype, int6
                          int num_heads, float softmax_scale, float* out, float* out_lse,
                          void* workspace, size_t workspace_bytes, int num_splits, int impl,
                          void* stream);
+// Where that call, on this workspace, keeps the e4m3 kernel's Q images: written
+// by the caller before it if `q_image_ready` is passed on; nullptr if the call
+// will not run that kernel.
+uint8_t* decode_chosen_q_image(int kv_dtype, int rows, int num_heads, int num_splits, int impl,
+                               void* workspace);
 int simt_sparse_chunk_max();
 cudaError_t launch_sparse_gather(const PartialParams& p, int row_bytes, int maxblk,
                                  uint8_t* gathered, int* counts, cudaStream_t st);

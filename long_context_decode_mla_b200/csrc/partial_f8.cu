@@ -1066,6 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1) partial_f8_kernel(const __grid_co
 // Q operand images of every request (q_image.cuh).  Grid (batch, 2): each CTA
 // covers 32 head rows with 8 threads per head.
 __global__ void __launch_bounds__(256) f8_q_image_kernel(const PartialParams p, uint8_t* image) {
+  ptx::launch_dependents();
   qimg::build_q_image_row(p.q, p.rows_q, p.heads, blockIdx.x,
                           blockIdx.y * 32 + (threadIdx.x >> 3), threadIdx.x & 7, image);
 }

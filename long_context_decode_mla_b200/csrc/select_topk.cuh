@@ -273,24 +273,5 @@ inline int cluster_size(long long n, int rows, int sms) {
   return size;
 }
 
-// Launches `kernel` with `rows` clusters of `size` CTAs (grid x = cluster rank).
-template <class... Args>
-cudaError_t launch(void (*kernel)(Args...), int rows, int size, size_t smem, cudaStream_t st,
-                   Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(size, rows);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = size;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace topk
 }  // namespace dcpmla

@@ -129,6 +129,20 @@ __device__ __forceinline__ bool mbar_wait4(uint64_t* const (&b)[4], const uint32
   return true;
 }
 
+// --------------------------------------------- programmatic dependent launch ----
+
+// Lets the next kernel of the stream start, if it was launched as a dependent.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Waits until the kernel this one was launched to depend on is complete and its
+// writes are visible (at once if there is none).  What was written before that
+// kernel started may be read earlier; what it writes is read with plain or .cg
+// loads, never through the read-only path.
+__device__ __forceinline__ void wait_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------- cp.async ----
 
 // 16-byte global -> shared copy; src_bytes = 0 zero-fills the destination.
