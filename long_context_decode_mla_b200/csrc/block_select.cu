@@ -31,13 +31,13 @@ namespace dcpmla {
 namespace {
 
 constexpr int kGroups = 5;
-constexpr int kTile = 64;                           // blocks per scoring tile
-constexpr uint32_t kChunk = 8192;                   // 64 rows x 128 bytes
+constexpr int kTile = 128;                          // blocks per scoring tile
+constexpr uint32_t kChunk = 8192;                   // 64 query rows x 128 bytes
 // Query image of a row: the int8 codes of 64 heads (zeros past the call's) in
 // the scoring kernel's shared-memory order, a 128-byte-swizzled chunk per
-// group (the rope's is half used), then the steps [64 heads][8] (5 used).
+// group (the rope's is half used), then the steps [group][head], 2 KB reserved.
 constexpr int kQCodes = kGroups * kChunk;
-constexpr int kQBytes = kQCodes + 64 * 8 * 4;
+constexpr int kQBytes = kQCodes + 2048;
 
 struct SelectParams {
   const __nv_bfloat16* q;      // [rows][heads][576]
@@ -53,7 +53,8 @@ struct SelectParams {
   uint8_t* q_image;            // the e4m3 decode kernel's Q images, or nullptr
   int num_ctas;                // SMs
   float* scores;               // [rows][tiles][heads][kTile]
-  uint32_t* tile_max;          // [rows][tiles][heads], as ordered keys
+  uint32_t* row_max;           // [rows][64] the heads' best scores, as ordered keys
+  uint32_t* keys;              // [rows][bt_stride] ranks, or nullptr: the chooser's own
   int* out_blocks;             // [rows][topk] or nullptr
   int* out_table;              // [rows][topk]
   int* out_lens;               // [rows]
@@ -126,7 +127,10 @@ __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParam
     *reinterpret_cast<uint32_t*>(out + at) = code;
   else
     *reinterpret_cast<uint16_t*>(out + at) = (uint16_t)code;
-  if (lane == 0) reinterpret_cast<float*>(out + kQCodes)[h * 8 + g] = step;
+  if (lane == 0) {
+    reinterpret_cast<float*>(out + kQCodes)[g * 64 + h] = step;
+    if (g == 0) p.row_max[(size_t)r * 64 + h] = 0u;      // below every score's key
+  }
   if (!p.q_image) return;
   any = __reduce_max_sync(0xffffffffu, any);
   if (lane == 0 && g < 4) top[half][g] = any;
@@ -148,27 +152,33 @@ __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParam
 
 // ----------------------------------------------------------- scoring ----
 //
-// Scores of tiles of 64 blocks on the tensor cores (tcgen05, kind::i8): the
-// summaries' codes are A (M = 64 blocks), the query's B (N = 64 heads), each
+// Scores of tiles of 128 blocks on the tensor cores (tcgen05, kind::i8): the
+// summaries' codes are A (M = 128 blocks), the query's B (N = 64 heads), each
 // scale group an int32 accumulator of its own, so that a TMEM lane holds one
-// block for 32 heads.  Summaries are scattered over the pool: four warps copy
-// them in 16-byte pieces (three tiles in flight) into swizzled chunks; warps
-// 0-3 and 4-7 turn alternate tiles into scores, written [head][block], and
-// the heads' maxima over the tile.  The tiles of all rows, end to end, are
-// dealt to the CTAs in contiguous ranges, so that a CTA rarely changes query.
-constexpr int kScoreThreads = 416;
-constexpr int kCopyBase = 256, kCopyThreads = 128, kMmaWarp = 12;
-constexpr int kScoreStages = 3, kBufs = 3;
-constexpr uint32_t kScaleBytes = 64 * 32;
-constexpr uint32_t kStageBytes = kGroups * kChunk + kScaleBytes;
-constexpr uint32_t kTmemCols = 512;
+// block for all heads.  Summaries are scattered over the pool: three warps copy
+// them in 16-byte pieces (two tiles in flight) into swizzled chunks; warps 0-3
+// and 4-7 add each group's product, scaled, into the scores of 32 heads a
+// thread, which are written [head][block], and keep each head's best of a row
+// until its end.  The tiles of all rows, end to end, are dealt to the CTAs in
+// contiguous ranges, so that a CTA rarely changes query.
+//
+// What bounds it is the load/store unit's queue (copies, stores, broadcast
+// reads) and the int8 MMAs, some 3,000 cycles each for 64 blocks: M = 64 tiles
+// with a warp maximum per head and tile took 4,300 cycles for them.
+constexpr int kScoreThreads = 384;       // twelve warps: 168 registers a thread
+constexpr int kCopyBase = 256, kCopyThreads = 96, kMmaWarp = 11;
+constexpr int kCopyRows = kCopyThreads / 16, kCopySteps = (kTile + kCopyRows - 1) / kCopyRows;
+constexpr int kScoreStages = 2, kBufs = 8;
+constexpr uint32_t kSlot = 2 * kChunk;             // 128 blocks x 128 bytes
+constexpr uint32_t kScaleBytes = kTile * 32;
+constexpr uint32_t kStageBytes = kGroups * kSlot + kScaleBytes;
+constexpr uint32_t kTmemCols = 64 * kBufs;
 constexpr int kRowChunk = 512;           // rows looked at together
 
 struct ScoreCtl {
   uint64_t full[kScoreStages], empty[kScoreStages];
   uint64_t d_full[kBufs], d_empty[kBufs];
   uint64_t q_full, q_empty;
-  uint32_t wmax[2][4][32];               // [group][warp of it][head of its half]
   uint32_t tmem_base;
   int abort;
   int warp_sums[16];
@@ -227,7 +237,7 @@ __device__ __forceinline__ float small_int(uint32_t x) {
   return __fsub_rn(__uint_as_float(0x4B400000u + x), 12582912.f);
 }
 
-// Copies of every tile (four warps) and of each row's query image.
+// Copies of every tile (three warps) and of each row's query image.
 __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, uint8_t* base, int r0,
                                           int lo, int hi, uint32_t& tau, uint32_t& sigma) {
   const int t = threadIdx.x - kCopyBase;
@@ -237,14 +247,14 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
   const int un0 = t & 15;
   // the tile's table entries, loaded a tile ahead: the copies of a tile would
   // otherwise wait for eight of them one after the other
-  int ids[8];
+  int ids[kCopySteps];
   auto entries = [&]() {
     const int* table =
         p.block_table + (size_t)((r0 + w.row) / p.q_len) * p.bt_stride + w.tile * kTile;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int row = (t >> 4) + 8 * k;
-      ids[k] = w.tile * kTile + row < w.nb ? __ldg(table + row) : 0;
+    for (int k = 0; k < kCopySteps; ++k) {
+      const int row = (t >> 4) + kCopyRows * k;
+      ids[k] = row < kTile && w.tile * kTile + row < w.nb ? __ldg(table + row) : 0;
     }
   };
   entries();
@@ -260,8 +270,8 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
     // sixteen lanes take a row's 38 pieces; rows past the tile's end are left
     // as they are (they only reach their own lanes)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int row = (t >> 4) + 8 * k;
+    for (int k = 0; k < kCopySteps; ++k) {
+      const int row = (t >> 4) + kCopyRows * k;
       if (row < n) {
         int blk = ids[k];
         if (blk < 0 || (long long)blk >= p.num_blocks) {
@@ -273,9 +283,9 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
         for (int j = 0; j < 3; ++j) {
           const int un = un0 + 16 * j;
           if (un < 36)
-            ptx::cp_async16(dst + (un >> 3) * kChunk + qimg::sw128(row, un & 7), src + 16 * un, 16);
+            ptx::cp_async16(dst + (un >> 3) * kSlot + qimg::sw128(row, un & 7), src + 16 * un, 16);
           else if (un < 38)
-            ptx::cp_async16(dst + kGroups * kChunk + row * 32 + (un - 36) * 16, src + 16 * un, 16);
+            ptx::cp_async16(dst + kGroups * kSlot + row * 32 + (un - 36) * 16, src + 16 * un, 16);
         }
       }
     }
@@ -299,34 +309,51 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
 }
 
 __device__ __forceinline__ void score_mma_role(ScoreCtl& c, uint8_t* base, int lo, int hi,
-                                               uint32_t& tau, uint32_t& sigma) {
-  constexpr uint32_t kId = ptx::idesc_i8(64, 64);
+                                               uint32_t& tau, uint32_t& sigma, uint32_t& part) {
+  constexpr uint32_t kId = ptx::idesc_i8(128, 64);
   const uint64_t dq = ptx::sdesc(ptx::smem_addr(base), 16, 1024, ptx::kSwizzle128B);
   const uint64_t dk0 = ptx::sdesc(ptx::smem_addr(base + kOffStage), 16, 1024, ptx::kSwizzle128B);
   TileWalk w;
   if (!w.start(c, lo, hi)) return;
   bool fresh = true;
   while (true) {
-    const uint32_t s = tau % kScoreStages, buf = tau % kBufs;
-    if (fresh) {
-      if (!ptx::mbar_wait(&c.q_full, sigma & 1, &c.abort)) return;
-      ++sigma;
-    }
-    if (tau >= (uint32_t)kBufs &&
-        !ptx::mbar_wait(&c.d_empty[buf], ((tau / kBufs) + 1) & 1, &c.abort))
-      return;
-    if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
-    ptx::tc_fence_after();
-    ptx::fence_proxy_async();      // the copies were made through the generic proxy
+    const uint32_t s = tau % kScoreStages;
+    if (fresh) ++sigma;
+    uint64_t* full = &c.full[s];
+    const uint32_t pf = (tau / kScoreStages) & 1;
     const uint64_t dk = dplus(dk0, s * kStageBytes);
-    const uint32_t d = c.tmem_base + buf * (32 * kGroups);
+    // one round trip tests the barriers of parts 0-1 with the tile's, then of 2-4
 #pragma unroll 1
-    for (int g = 0; g < kGroups; ++g)
-      for (int ks = 0; ks < (g < 4 ? 4 : 2); ++ks)
-        ptx::mma_ws_i8(d + 32 * g, dplus(dk, g * kChunk + ks * 32), dplus(dq, g * kChunk + ks * 32),
-                       kId, ks > 0);
+    for (int g0 = 0; g0 < kGroups; g0 += g0 == 0 ? 2 : 3) {
+      const int n = g0 == 0 ? 2 : 3;
+      uint64_t* bars[4];
+      uint32_t pars[4];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t pi = part + (i < n ? i : 0);
+        const bool reuse = pi >= (uint32_t)kBufs;
+        bars[i] = reuse ? &c.d_empty[pi % kBufs] : full;
+        pars[i] = reuse ? ((pi / kBufs) + 1) & 1 : pf;
+      }
+      if (g0 == 0) {
+        bars[2] = &c.q_full;
+        pars[2] = (sigma - 1) & 1;
+      }
+      bars[3] = full;
+      pars[3] = pf;
+      if (!ptx::mbar_wait4(bars, pars, &c.abort)) return;
+      ptx::tc_fence_after();
+      ptx::fence_proxy_async();      // the copies were made through the generic proxy
+#pragma unroll 1
+      for (int g = g0; g < g0 + n; ++g, ++part) {
+        const uint32_t d = c.tmem_base + 64 * (part % kBufs);
+        for (int ks = 0; ks < (g < 4 ? 4 : 2); ++ks)
+          ptx::mma_i8(d, dplus(dk, g * kSlot + ks * 32), dplus(dq, g * kChunk + ks * 32), kId,
+                      ks > 0);
+        ptx::mma_commit(&c.d_full[part % kBufs]);
+      }
+    }
     ptx::mma_commit(&c.empty[s]);
-    ptx::mma_commit(&c.d_full[buf]);
     fresh = w.last_of_row();
     if (fresh) ptx::mma_commit(&c.q_empty);
     ++tau;
@@ -334,82 +361,82 @@ __device__ __forceinline__ void score_mma_role(ScoreCtl& c, uint8_t* base, int l
   }
 }
 
+// Scores: thread (hh, row) has heads [32 hh, 32 hh + 32) of the tile's block.
 __device__ __forceinline__ void score_role(const SelectParams& p, ScoreCtl& c, uint8_t* base, int r0,
-                                           int lo, int hi, uint32_t& tau, uint32_t& sigma) {
-  const int group = threadIdx.x >> 7, t = threadIdx.x & 127;
-  const int row = t & 63, hh = t >> 6, lane = t & 31, warp = t >> 5;
-  const uint32_t lane_base = c.tmem_base + ((uint32_t)(warp * 32) << 16);
-  const float* steps = reinterpret_cast<const float*>(base + kQCodes);
+                                           int lo, int hi, uint32_t& tau, uint32_t& sigma,
+                                           uint32_t& part) {
+  const int hh = threadIdx.x >> 7, row = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t lane_base = c.tmem_base + ((uint32_t)((row >> 5) * 32) << 16) + 32 * hh;
+  const float* steps = reinterpret_cast<const float*>(base + kQCodes) + 32 * hh;
+  const int heads = min(32, p.heads - 32 * hh);      // of this thread (may be <= 0)
   TileWalk w;
   if (!w.start(c, lo, hi)) return;
   bool fresh = true;
+  float best[32];
   while (true) {
     if (fresh) {
-      // both groups follow every row, so that each knows which image is in place
       if (!ptx::mbar_wait(&c.q_full, sigma & 1, &c.abort)) return;
       ++sigma;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) best[e] = -INFINITY;
     }
     fresh = w.last_of_row();
-    if ((int)(tau & 1) == group) {
-      const uint32_t s = tau % kScoreStages, buf = tau % kBufs;
-      const int r = r0 + w.row, k = w.tile * kTile + row;
-      bool live = k < w.nb;
-      if (live) {
-        const int blk = __ldg(p.block_table + (size_t)(r / p.q_len) * p.bt_stride + k);
-        live = blk >= 0 && (long long)blk < p.num_blocks;
-      }
-      if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
-      const uint8_t* sp = base + kOffStage + s * kStageBytes + kGroups * kChunk + row * 32;
-      const float4 s4 = *reinterpret_cast<const float4*>(sp);
-      const float sc[kGroups] = {s4.x, s4.y, s4.z, s4.w, *reinterpret_cast<const float*>(sp + 16)};
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&c.empty[s]);
-      if (!ptx::mbar_wait(&c.d_full[buf], (tau / kBufs) & 1, &c.abort)) return;
+    const uint32_t s = tau % kScoreStages;
+    const int r = r0 + w.row, k = w.tile * kTile + row;
+    bool live = k < w.nb;
+    if (live) {
+      const int blk = __ldg(p.block_table + (size_t)(r / p.q_len) * p.bt_stride + k);
+      live = blk >= 0 && (long long)blk < p.num_blocks;
+    }
+    if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
+    const uint8_t* sp = base + kOffStage + s * kStageBytes + kGroups * kSlot + row * 32;
+    const float4 s4 = *reinterpret_cast<const float4*>(sp);
+    const float sc[kGroups] = {s4.x, s4.y, s4.z, s4.w, *reinterpret_cast<const float*>(sp + 16)};
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&c.empty[s]);
+    float v[32];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g, ++part) {
+      const uint32_t buf = part % kBufs;
+      if (!ptx::mbar_wait(&c.d_full[buf], (part / kBufs) & 1, &c.abort)) return;
       __syncwarp();
       ptx::tc_fence_after();
-      float* out = p.scores + ((size_t)r * p.tiles + w.tile) * p.heads * kTile + row;
+      uint32_t x[32];
+      ptx::tmem_ld32(lane_base + 64 * buf, x);
+      ptx::tmem_wait_ld();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&c.d_empty[buf]);
 #pragma unroll
-      for (int piece = 0; piece < 2; ++piece) {
-        const int h0 = 32 * hh + 16 * piece;
-        uint32_t x[kGroups][16];
+      for (int e4 = 0; e4 < 8; ++e4) {
+        const float4 q4 = *reinterpret_cast<const float4*>(steps + g * 64 + 4 * e4);
+        const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-          ptx::tmem_ld16(lane_base + buf * (32 * kGroups) + 32 * g + 16 * piece, x[g]);
-        ptx::tmem_wait_ld();
-        if (piece == 1) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&c.d_empty[buf]);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (h0 + e < p.heads) {
-            const float4 q4 = *reinterpret_cast<const float4*>(steps + (h0 + e) * 8);
-            const float q5 = steps[(h0 + e) * 8 + 4];
-            const float qs[kGroups] = {q4.x, q4.y, q4.z, q4.w, q5};
-            float v = 0.f;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-              const float term = __fmul_rn(small_int(x[g][e]), __fmul_rn(qs[g], sc[g]));
-              v = g == 0 ? term : __fadd_rn(v, term);
-            }
-            if (!live) v = -INFINITY;
-            out[(size_t)(h0 + e) * kTile] = v;
-            const uint32_t m = __reduce_max_sync(0xffffffffu, topk::key_of(v));
-            if (lane == 0) c.wmax[group][warp][16 * piece + e] = m;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * e4 + i;
+          const float term = __fmul_rn(small_int(x[e]), __fmul_rn(qs[i], sc[g]));
+          v[e] = g == 0 ? term : __fadd_rn(v[e], term);
         }
       }
-      ptx::named_bar(1 + group, 128);
-      if (t < p.heads)
-        p.tile_max[((size_t)r * p.tiles + w.tile) * p.heads + t] =
-            max(c.wmax[group][2 * (t >> 5)][t & 31], c.wmax[group][2 * (t >> 5) + 1][t & 31]);
-      ptx::named_bar(1 + group, 128);
     }
-    // the row's steps are read (both groups arrive, once a row)
+    float* out = p.scores + (((size_t)r * p.tiles + w.tile) * p.heads + 32 * hh) * kTile + row;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      if (!live) v[e] = -INFINITY;
+      best[e] = fmaxf(best[e], v[e]);
+      if (e < heads) out[e * kTile] = v[e];
+    }
     if (fresh) {
+      // the row's image is done with here; its heads' best go to the row
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&c.q_empty);
+      uint32_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, topk::key_of(best[e]));
+        if (lane == e) mine = m;
+      }
+      if (lane < heads) atomicMax(p.row_max + (size_t)r * 64 + 32 * hh + lane, mine);
     }
     ++tau;
     if (!w.next(c)) break;
@@ -426,11 +453,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   if (threadIdx.x == 0) {
     for (int s = 0; s < kScoreStages; ++s) {
       ptx::mbar_init(&c.full[s], kCopyThreads);
-      ptx::mbar_init(&c.empty[s], 5);        // the MMAs' commit, four warps' scale reads
+      ptx::mbar_init(&c.empty[s], 1 + 8);    // the MMAs' commit, eight warps' scale reads
     }
     for (int k = 0; k < kBufs; ++k) {
       ptx::mbar_init(&c.d_full[k], 1);
-      ptx::mbar_init(&c.d_empty[k], 4);
+      ptx::mbar_init(&c.d_empty[k], 8);
     }
     ptx::mbar_init(&c.q_full, 1);
     ptx::mbar_init(&c.q_empty, 1 + 8);       // the MMAs' commit, eight warps' step reads
@@ -443,7 +470,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   __syncthreads();
   ptx::tc_fence_after();
   const int rows = p.batch * p.q_len;
-  uint32_t tau = 0, sigma = 0;
+  uint32_t tau = 0, sigma = 0, part = 0;
   for (int r0 = 0; r0 < rows; r0 += kRowChunk) {
     int total = 0;
     for (int i0 = 0; i0 < kRowChunk; i0 += kScoreThreads) {
@@ -463,11 +490,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
     const int lo = (int)((long long)blockIdx.x * total / gridDim.x);
     const int hi = (int)((long long)(blockIdx.x + 1) * total / gridDim.x);
     if (warp < 8) {
-      score_role(p, c, base, r0, lo, hi, tau, sigma);
+      score_role(p, c, base, r0, lo, hi, tau, sigma, part);
     } else if (warp < kMmaWarp) {
       copy_role(p, c, base, r0, lo, hi, tau, sigma);
     } else {
-      if ((threadIdx.x & 31) == 0) score_mma_role(c, base, lo, hi, tau, sigma);
+      if ((threadIdx.x & 31) == 0) score_mma_role(c, base, lo, hi, tau, sigma, part);
     }
     __syncthreads();
     if (c.abort) break;
@@ -475,13 +502,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   // a CTA without tiles waits too: this kernel's end implies the previous one's
   ptx::wait_primary();
   // Drain: every asynchronous arrival and copy lands before the CTA exits.
-  if (threadIdx.x == kMmaWarp * 32) {
+  if (warp >= kMmaWarp && (threadIdx.x & 31) == 0) {
     for (uint32_t s = 0; s < (uint32_t)kScoreStages; ++s) {
       const uint32_t u = tau > s ? (tau - s + kScoreStages - 1) / kScoreStages : 0;
       if (u > 0) ptx::mbar_wait(&c.empty[s], (u - 1) & 1, &c.abort);
     }
     for (uint32_t k = 0; k < (uint32_t)kBufs; ++k) {
-      const uint32_t u = tau > k ? (tau - k + kBufs - 1) / kBufs : 0;
+      const uint32_t u = part > k ? (part - k + kBufs - 1) / kBufs : 0;
       if (u > 0) ptx::mbar_wait(&c.d_full[k], (u - 1) & 1, &c.abort);
     }
     if (sigma > 0) ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort);
@@ -498,12 +525,49 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   if (warp == 0) ptx::tmem_dealloc(c.tmem_base, kTmemCols);
 }
 
-// Ranks and the choice of one row: one cluster.
+// Key of block k of a row: its rank, or the largest key where it is taken anyway.
+__device__ __forceinline__ uint32_t rank_key(const SelectParams& p, const float* hmax, int r, int k,
+                                             int nb) {
+  if (nb <= p.topk || k < p.sink || k >= nb - p.recent) return 0xFFFFFFFFu;
+  const float* s = p.scores + ((size_t)r * p.tiles + k / kTile) * p.heads * kTile + k % kTile;
+  float rank = -INFINITY;
+  auto add = [&](float v, int h) {
+    // equal infinities: no distance
+    rank = fmaxf(rank, v == hmax[h] ? 0.f : __fsub_rn(v, hmax[h]));
+  };
+  int h = 0;
+  for (; h + 16 <= p.heads; h += 16) {
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __ldcg(s + (h + e) * kTile);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) add(v[e], h + e);
+  }
+  for (; h < p.heads; ++h) add(__ldcg(s + h * kTile), h);
+  return topk::key_of(rank);
+}
+
+// Ranks of long rows, all over the device (a row's scores are 256 bytes a block
+// and head set: read by its cluster alone, 16,384 blocks took 20 us).
+constexpr int kRankThreads = 256;
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const SelectParams p) {
+  __shared__ float hmax[64];
+  ptx::launch_dependents();
+  const int r = blockIdx.y, k = blockIdx.x * kRankThreads + threadIdx.x;
+  int nb;
+  rows_of(p, r, &nb);
+  ptx::wait_primary();
+  if (blockIdx.x * kRankThreads >= nb) return;
+  if (threadIdx.x < 64) hmax[threadIdx.x] = topk::value_of(__ldcg(p.row_max + r * 64 + threadIdx.x));
+  __syncthreads();
+  if (k < nb) p.keys[(size_t)r * p.bt_stride + k] = rank_key(p, hmax, r, k, nb);
+}
+
+// Ranks (unless there) and the choice of one row: one cluster.
 __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectParams p, int bit_words) {
   extern __shared__ __align__(16) uint32_t dyn[];
   __shared__ topk::Ctl c;
   __shared__ float hmax[64];
-  __shared__ uint32_t kmax[64];
   topk::cg::cluster_group cl = topk::cg::this_cluster();
   const int r = blockIdx.y, b = r / p.q_len;
   int nb;
@@ -514,44 +578,10 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   topk::slice(nb, cl.block_rank(), cl.num_blocks(), &lo, &hi);
   const int want = min(nb, p.topk);
   ptx::wait_primary();
-  const int tiles = (nb + kTile - 1) / kTile;
-  if (threadIdx.x < 64) kmax[threadIdx.x] = 0;
+  if (threadIdx.x < 64) hmax[threadIdx.x] = topk::value_of(__ldcg(p.row_max + r * 64 + threadIdx.x));
   __syncthreads();
-  {
-    const uint32_t* tm = p.tile_max + (size_t)r * p.tiles * p.heads;
-    const int h = threadIdx.x & 63, t0 = threadIdx.x >> 6;
-    uint32_t m = 0;
-    if (h < p.heads && nb > p.topk) {
-#pragma unroll 4
-      for (int t = t0; t < tiles; t += topk::kThreads / 64) m = max(m, __ldcg(tm + t * p.heads + h));
-      atomicMax(&kmax[h], m);
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x < 64) hmax[threadIdx.x] = topk::value_of(kmax[threadIdx.x]);
-  __syncthreads();
-  for (int k = lo + threadIdx.x; k < hi; k += topk::kThreads) {
-    uint32_t key = 0xFFFFFFFFu;
-    if (nb > p.topk && k >= p.sink && k < nb - p.recent) {
-      const float* s = p.scores + ((size_t)r * p.tiles + k / kTile) * p.heads * kTile + k % kTile;
-      float rank = -INFINITY;
-      auto add = [&](float v, int h) {
-        // equal infinities: no distance
-        rank = fmaxf(rank, v == hmax[h] ? 0.f : __fsub_rn(v, hmax[h]));
-      };
-      int h = 0;
-      for (; h + 16 <= p.heads; h += 16) {
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __ldcg(s + (h + e) * kTile);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) add(v[e], h + e);
-      }
-      for (; h < p.heads; ++h) add(__ldcg(s + h * kTile), h);
-      key = topk::key_of(rank);
-    }
-    keys[k - lo] = key;
-  }
+  for (int k = lo + threadIdx.x; k < hi; k += topk::kThreads)
+    keys[k - lo] = p.keys ? __ldcg(p.keys + (size_t)r * p.bt_stride + k) : rank_key(p, hmax, r, k, nb);
   __syncthreads();
   if (want > 0)
     topk::mark(cl, c, lo, hi, want, bits, [&](int i, bool) { return keys[i - lo]; });
@@ -585,17 +615,21 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Workspace: 256-byte header (flag word), q codes, scores, tile maxima.
+// Rows of more blocks than this are ranked by a kernel of its own.
+constexpr int kRankStride = 4096;
+
+// Workspace: 256-byte header (flag word), q codes, scores, the heads' best, keys.
 struct SelectLayout {
-  size_t q_codes, scores, tile_max, total;
+  size_t q_codes, scores, row_max, keys, total;
 };
 SelectLayout layout(int rows, int heads, int stride) {
   const size_t tiles = ((size_t)stride + kTile - 1) / kTile;
   SelectLayout l;
   l.q_codes = kWsHeader;
   l.scores = l.q_codes + round256((size_t)rows * kQBytes);
-  l.tile_max = l.scores + round256((size_t)rows * tiles * heads * kTile * 4);
-  l.total = l.tile_max + round256((size_t)rows * tiles * heads * 4);
+  l.row_max = l.scores + round256((size_t)rows * tiles * heads * kTile * 4);
+  l.keys = l.row_max + (size_t)rows * 256;
+  l.total = l.keys + (stride > kRankStride ? round256((size_t)rows * stride * 4) : 0);
   return l;
 }
 
@@ -678,6 +712,11 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   e = launch_kernel(score_kernel, dim3((unsigned)std::min<long long>(p.num_ctas, (long long)rows * p.tiles)),
                     kScoreThreads, kScoreSmem, st, 0, true, p);
   if (e != cudaSuccess) return e;
+  if (p.keys) {
+    e = launch_kernel(rank_kernel, dim3((p.bt_stride + kRankThreads - 1) / kRankThreads, rows),
+                      kRankThreads, 0, st, 0, true, p);
+    if (e != cudaSuccess) return e;
+  }
   int size = topk::cluster_size(p.bt_stride, rows, p.num_ctas);
   while ((long long)size * kMaxKeys < p.bt_stride) size *= 2;      // keys and bits in shared memory
   const int words = topk::slice_words(p.bt_stride, size);
@@ -696,7 +735,8 @@ int run_select(SelectParams& p, uint8_t* ws, cudaStream_t st) {
   const SelectLayout l = layout(p.batch * p.q_len, p.heads, p.bt_stride);
   p.q_codes = ws + l.q_codes;
   p.scores = reinterpret_cast<float*>(ws + l.scores);
-  p.tile_max = reinterpret_cast<uint32_t*>(ws + l.tile_max);
+  p.row_max = reinterpret_cast<uint32_t*>(ws + l.row_max);
+  p.keys = p.bt_stride > kRankStride ? reinterpret_cast<uint32_t*>(ws + l.keys) : nullptr;
   return launch_select(p, st) == cudaSuccess ? DCPMLA_OK : DCPMLA_ERR_CUDA;
 }
 
@@ -788,17 +828,29 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
   rc = mla_decode_workspace_size(rows, num_heads, num_splits, 0, &dec);
   if (rc != DCPMLA_OK) return rc;
   uint8_t* sel = static_cast<uint8_t*>(workspace) + round256(dec);
+  // With fewer chosen blocks than CTAs a CTA takes two of them, down to sixteen
+  // pieces a query: half the pieces to combine (one request of 64 blocks: 79 us
+  // with 64 pieces, 74 with 32, 76 with 16; the workspace has room for more).
+  int splits = num_splits;
+  if (splits == 0) {
+    int sms = 0;
+    rc = dcpmla_device_sm_count(&sms);
+    if (rc != DCPMLA_OK) return rc;
+    const long long tiles = (long long)rows * block_topk;
+    splits = (int)std::min<long long>(
+        sms, std::max<long long>((long long)rows * std::min(block_topk, 16), (tiles + 1) / 2));
+  }
   p.out_blocks = out_blocks;
   p.out_table = reinterpret_cast<int*>(sel + layout(rows, num_heads, block_table_stride).total);
   p.out_lens = p.out_table + round256((size_t)rows * block_topk * 4) / 4;
   p.flags = static_cast<int*>(workspace);
-  p.q_image = decode_chosen_q_image(kv_dtype, rows, num_heads, num_splits, impl, workspace);
+  p.q_image = decode_chosen_q_image(kv_dtype, rows, num_heads, splits, impl, workspace);
   rc = run_select(p, sel, static_cast<cudaStream_t>(stream));
   if (rc != DCPMLA_OK) return rc;
   // the chosen blocks of a query are one request of one shard, in a table of their own
   return decode_chosen_blocks(q, kv_cache, kv_dtype, num_blocks, p.out_table, block_topk,
                               p.out_lens, rows, num_heads, softmax_scale, out_partial, out_lse,
-                              workspace, dec, num_splits, impl, stream);
+                              workspace, dec, splits, impl, stream);
 }
 
 }  // extern "C"

@@ -280,12 +280,12 @@ __device__ __forceinline__ void mma_ws_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// Weight-stationary int8 form (kind::i8, int32 accumulation: exact).
-__device__ __forceinline__ void mma_ws_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
+// cta_group::1 kind::i8 (non weight-stationary; int32 accumulation: exact).
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.ws.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
