@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParam
 // Scores of tiles of 128 blocks on the tensor cores (tcgen05, kind::i8): the
 // summaries' codes are A (M = 128 blocks), the query's B (N = 64 heads), each
 // scale group an int32 accumulator of its own, so that a TMEM lane holds one
-// block for all heads.  Summaries are scattered over the pool: three warps copy
-// them in 16-byte pieces (two tiles in flight) into swizzled chunks; warps 0-3
+// block for all heads.  Summaries are scattered over the pool: seven warps bring
+// them in 16-byte pieces into swizzled chunks (two tiles); warps 0-3
 // and 4-7 add each group's product, scaled, into the scores of 32 heads a
 // thread, which are written [head][block], and keep each head's best of a row
 // until its end.  The tiles of all rows, end to end, are dealt to the CTAs in
@@ -165,20 +165,29 @@ __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParam
 // What bounds it is the load/store unit's queue (copies, stores, broadcast
 // reads) and the int8 MMAs, some 3,000 cycles each for 64 blocks: M = 64 tiles
 // with a warp maximum per head and tile took 4,300 cycles for them.
-constexpr int kScoreThreads = 384;       // twelve warps: 168 registers a thread
-constexpr int kCopyBase = 256, kCopyThreads = 96, kMmaWarp = 11;
-constexpr int kCopyRows = kCopyThreads / 16, kCopySteps = (kTile + kCopyRows - 1) / kCopyRows;
+// Sixteen warps: eight score, seven copy, one issues the MMAs; the launch gives a
+// thread 128 registers, of which the scoring warpgroups take from the others.
+constexpr int kScoreThreads = 512;
+constexpr int kCopyBase = 256, kCopyThreads = 224, kMmaWarp = 15;
+constexpr int kBarCopy = 1;
+constexpr int kLaunchRegs = 128, kScoreRegs = 168, kCopyRegs = 88;
+static_assert(256 * (kScoreRegs + kCopyRegs) == kScoreThreads * kLaunchRegs,
+              "the register split must add up to what the launch holds");
+constexpr int kUnits = kSummaryBytes / 16;         // 16-byte pieces of a summary
+constexpr int kCopyBatch = 11;                     // pieces a thread has in flight
+constexpr int kCopyBatches = (kTile * kUnits + kCopyThreads * kCopyBatch - 1) / (kCopyThreads * kCopyBatch);
 constexpr int kScoreStages = 2, kBufs = 8;
 constexpr uint32_t kSlot = 2 * kChunk;             // 128 blocks x 128 bytes
 constexpr uint32_t kScaleBytes = kTile * 32;
 constexpr uint32_t kStageBytes = kGroups * kSlot + kScaleBytes;
 constexpr uint32_t kTmemCols = 64 * kBufs;
-constexpr int kRowChunk = 512;           // rows looked at together
+constexpr int kRowChunk = kScoreThreads; // rows looked at together
 
 struct ScoreCtl {
   uint64_t full[kScoreStages], empty[kScoreStages];
   uint64_t d_full[kBufs], d_empty[kBufs];
   uint64_t q_full, q_empty;
+  int ids[2][kTile];                     // the blocks of a tile, by tile parity
   uint32_t tmem_base;
   int abort;
   int warp_sums[16];
@@ -237,59 +246,73 @@ __device__ __forceinline__ float small_int(uint32_t x) {
   return __fsub_rn(__uint_as_float(0x4B400000u + x), 12582912.f);
 }
 
-// Copies of every tile (three warps) and of each row's query image.
+// Copies of every tile (seven warps) and of each row's query image.  A tile's
+// summaries are 128 x 38 pieces, dealt to the threads in order, so that a warp
+// reads 512 bytes that mostly follow one another; a batch of them is in flight a
+// thread, the first before the stage is known to be free.  (Asynchronous 16-byte
+// copies took 40 cycles of the unit each, 8,000 a tile.)
 __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, uint8_t* base, int r0,
                                           int lo, int hi, uint32_t& tau, uint32_t& sigma) {
   const int t = threadIdx.x - kCopyBase;
   TileWalk w;
   if (!w.start(c, lo, hi)) return;
   bool fresh = true;
-  const int un0 = t & 15;
-  // the tile's table entries, loaded a tile ahead: the copies of a tile would
-  // otherwise wait for eight of them one after the other
-  int ids[kCopySteps];
-  auto entries = [&]() {
-    const int* table =
-        p.block_table + (size_t)((r0 + w.row) / p.q_len) * p.bt_stride + w.tile * kTile;
-#pragma unroll
-    for (int k = 0; k < kCopySteps; ++k) {
-      const int row = (t >> 4) + kCopyRows * k;
-      ids[k] = row < kTile && w.tile * kTile + row < w.nb ? __ldg(table + row) : 0;
-    }
+  // the block of row t of the walk's tile; a bad entry: a stand-in, flagged
+  auto entry = [&]() {
+    const int k = w.tile * kTile + t;
+    if (t >= kTile || k >= w.nb) return 0;
+    const int blk = __ldg(p.block_table + (size_t)((r0 + w.row) / p.q_len) * p.bt_stride + k);
+    if (blk >= 0 && (long long)blk < p.num_blocks) return blk;
+    if (p.flags) atomicOr(p.flags, kFlagBadBlock);
+    return 0;
   };
-  entries();
+  if (t < kTile) c.ids[tau & 1][t] = entry();
+  ptx::named_bar(kBarCopy, kCopyThreads);
   while (true) {
     const uint32_t s = tau % kScoreStages;
-    if (tau >= (uint32_t)kScoreStages &&
-        !ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort))
-      return;
+    const int* ids = c.ids[tau & 1];
     const int r = r0 + w.row;
+    // rows past the tile's end are left as they are (they only reach their own lanes)
+    const int units = min(kTile, w.nb - w.tile * kTile) * kUnits;
+    const bool row_ends = w.last_of_row();
+    const bool more = w.next(c);
+    const int next_id = more ? entry() : 0;
+    if (more && t < kTile && w.tile * kTile + t < w.nb) {
+      // the next tile's lines on their way to L2: a batch then waits a third as long
+      const uint8_t* src = p.summaries + (size_t)next_id * kSummaryBytes;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) ptx::prefetch_line_l2(src + 128 * i);
+    }
     uint8_t* stage = base + kOffStage + s * kStageBytes;
-    const uint32_t dst = ptx::smem_addr(stage);
-    const int n = min(kTile, w.nb - w.tile * kTile);
-    // sixteen lanes take a row's 38 pieces; rows past the tile's end are left
-    // as they are (they only reach their own lanes)
+#pragma unroll 1
+    for (int b = 0; b < kCopyBatches; ++b) {
+      uint4 v[kCopyBatch];
 #pragma unroll
-    for (int k = 0; k < kCopySteps; ++k) {
-      const int row = (t >> 4) + kCopyRows * k;
-      if (row < n) {
-        int blk = ids[k];
-        if (blk < 0 || (long long)blk >= p.num_blocks) {
-          if (un0 == 0 && p.flags) atomicOr(p.flags, kFlagBadBlock);
-          blk = 0;
+      for (int i = 0; i < kCopyBatch; ++i) {
+        const int u = t + kCopyThreads * (b * kCopyBatch + i);
+        if (u < units) {
+          const int row = u / kUnits;
+          v[i] = __ldg(reinterpret_cast<const uint4*>(
+                           p.summaries + (size_t)ids[row] * kSummaryBytes) + (u - row * kUnits));
         }
-        const uint8_t* src = p.summaries + (size_t)blk * kSummaryBytes;
+      }
+      if (b == 0 && tau >= (uint32_t)kScoreStages &&
+          !ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort))
+        return;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const int un = un0 + 16 * j;
-          if (un < 36)
-            ptx::cp_async16(dst + (un >> 3) * kSlot + qimg::sw128(row, un & 7), src + 16 * un, 16);
-          else if (un < 38)
-            ptx::cp_async16(dst + kGroups * kSlot + row * 32 + (un - 36) * 16, src + 16 * un, 16);
+      for (int i = 0; i < kCopyBatch; ++i) {
+        const int u = t + kCopyThreads * (b * kCopyBatch + i);
+        if (u < units) {
+          const int row = u / kUnits, un = u - row * kUnits;
+          *reinterpret_cast<uint4*>(stage + (un < 36 ? (un >> 3) * kSlot + qimg::sw128(row, un & 7)
+                                                     : kGroups * kSlot + row * 32 + (un - 36) * 16)) =
+              v[i];
         }
       }
     }
-    ptx::cp_async_arrive(&c.full[s]);
+    ptx::fence_proxy_async();          // the MMAs read through the async proxy
+    __syncwarp();
+    if ((t & 31) == 0) ptx::mbar_arrive(&c.full[s]);
     if (fresh) {
       if (t == 0) {
         if (sigma > 0 && !ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort)) return;
@@ -301,10 +324,11 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
       }
       ++sigma;
     }
-    fresh = w.last_of_row();
+    fresh = row_ends;
     ++tau;
-    if (!w.next(c)) break;
-    entries();
+    if (!more) break;
+    if (t < kTile) c.ids[tau & 1][t] = next_id;
+    ptx::named_bar(kBarCopy, kCopyThreads);
   }
 }
 
@@ -343,7 +367,6 @@ __device__ __forceinline__ void score_mma_role(ScoreCtl& c, uint8_t* base, int l
       pars[3] = pf;
       if (!ptx::mbar_wait4(bars, pars, &c.abort)) return;
       ptx::tc_fence_after();
-      ptx::fence_proxy_async();      // the copies were made through the generic proxy
 #pragma unroll 1
       for (int g = g0; g < g0 + n; ++g, ++part) {
         const uint32_t d = c.tmem_base + 64 * (part % kBufs);
@@ -443,6 +466,71 @@ __device__ __forceinline__ void score_role(const SelectParams& p, ScoreCtl& c, u
   }
 }
 
+// Barrier over the whole block, written out so that the two sides of the register
+// split can both use it.
+__device__ __forceinline__ void block_bar() { ptx::named_bar(2, kScoreThreads); }
+
+// The chunks of rows, on one side of the register split: kScorers the scoring
+// warps, else the copies and the MMAs and, at the end, the drains.  Both take the
+// same block barriers.
+template <bool kScorers>
+__device__ __forceinline__ void run_scores(const SelectParams& p, ScoreCtl& c, uint8_t* base) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = p.batch * p.q_len;
+  uint32_t tau = 0, sigma = 0, part = 0;
+  for (int r0 = 0; r0 < rows; r0 += kRowChunk) {
+    // a row a thread (kRowChunk = kScoreThreads): tiles, and their running sum
+    int nb = 0;
+    if (r0 + (int)threadIdx.x < rows) rows_of(p, r0 + threadIdx.x, &nb);
+    const int nt = nb > p.topk ? (nb + kTile - 1) / kTile : 0;     // else all are taken
+    int x = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) c.warp_sums[warp] = x;
+    block_bar();
+    int total = 0;
+#pragma unroll
+    for (int k = 0; k < kScoreThreads / 32; ++k) {
+      if (k < warp) x += c.warp_sums[k];
+      total += c.warp_sums[k];
+    }
+    c.end[threadIdx.x] = x;
+    c.blocks[threadIdx.x] = nb;
+    block_bar();
+    const int lo = (int)((long long)blockIdx.x * total / gridDim.x);
+    const int hi = (int)((long long)(blockIdx.x + 1) * total / gridDim.x);
+    if constexpr (kScorers) {
+      score_role(p, c, base, r0, lo, hi, tau, sigma, part);
+    } else {
+      if (warp < kMmaWarp)
+        copy_role(p, c, base, r0, lo, hi, tau, sigma);
+      else if (lane == 0)
+        score_mma_role(c, base, lo, hi, tau, sigma, part);
+    }
+    block_bar();
+    if (c.abort) break;
+  }
+  if constexpr (!kScorers) {
+    // Drain: every asynchronous arrival and copy lands before the CTA exits.
+    if (threadIdx.x == kMmaWarp * 32) {
+      for (uint32_t s = 0; s < (uint32_t)kScoreStages; ++s) {
+        const uint32_t u = tau > s ? (tau - s + kScoreStages - 1) / kScoreStages : 0;
+        if (u > 0) ptx::mbar_wait(&c.empty[s], (u - 1) & 1, &c.abort);
+      }
+      for (uint32_t k = 0; k < (uint32_t)kBufs; ++k) {
+        const uint32_t u = part > k ? (part - k + kBufs - 1) / kBufs : 0;
+        if (u > 0) ptx::mbar_wait(&c.d_full[k], (u - 1) & 1, &c.abort);
+      }
+      if (sigma > 0) ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort);
+    }
+    if (threadIdx.x == kCopyBase && sigma > 0)
+      ptx::mbar_wait(&c.q_full, (sigma - 1) & 1, &c.abort);
+  }
+}
+
 __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -452,7 +540,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   ptx::launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kScoreStages; ++s) {
-      ptx::mbar_init(&c.full[s], kCopyThreads);
+      ptx::mbar_init(&c.full[s], kCopyThreads / 32);
       ptx::mbar_init(&c.empty[s], 1 + 8);    // the MMAs' commit, eight warps' scale reads
     }
     for (int k = 0; k < kBufs; ++k) {
@@ -469,55 +557,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const int rows = p.batch * p.q_len;
-  uint32_t tau = 0, sigma = 0, part = 0;
-  for (int r0 = 0; r0 < rows; r0 += kRowChunk) {
-    int total = 0;
-    for (int i0 = 0; i0 < kRowChunk; i0 += kScoreThreads) {
-      const int i = i0 + threadIdx.x;
-      int nb = 0;
-      if (i < kRowChunk && r0 + i < rows) rows_of(p, r0 + i, &nb);
-      const int nt = nb > p.topk ? (nb + kTile - 1) / kTile : 0;    // else all are taken
-      int tot;
-      const int ex = block_exclusive_scan(nt, c.warp_sums, &tot);
-      if (i < kRowChunk) {
-        c.end[i] = total + ex + nt;
-        c.blocks[i] = nb;
-      }
-      total += tot;
-    }
-    __syncthreads();
-    const int lo = (int)((long long)blockIdx.x * total / gridDim.x);
-    const int hi = (int)((long long)(blockIdx.x + 1) * total / gridDim.x);
-    if (warp < 8) {
-      score_role(p, c, base, r0, lo, hi, tau, sigma, part);
-    } else if (warp < kMmaWarp) {
-      copy_role(p, c, base, r0, lo, hi, tau, sigma);
-    } else {
-      if ((threadIdx.x & 31) == 0) score_mma_role(c, base, lo, hi, tau, sigma, part);
-    }
-    __syncthreads();
-    if (c.abort) break;
+  // every warpgroup adjusts its registers here, before any role can return
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScoreRegs));
+    run_scores<true>(p, c, base);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+    run_scores<false>(p, c, base);
   }
   // a CTA without tiles waits too: this kernel's end implies the previous one's
   ptx::wait_primary();
-  // Drain: every asynchronous arrival and copy lands before the CTA exits.
-  if (warp >= kMmaWarp && (threadIdx.x & 31) == 0) {
-    for (uint32_t s = 0; s < (uint32_t)kScoreStages; ++s) {
-      const uint32_t u = tau > s ? (tau - s + kScoreStages - 1) / kScoreStages : 0;
-      if (u > 0) ptx::mbar_wait(&c.empty[s], (u - 1) & 1, &c.abort);
-    }
-    for (uint32_t k = 0; k < (uint32_t)kBufs; ++k) {
-      const uint32_t u = part > k ? (part - k + kBufs - 1) / kBufs : 0;
-      if (u > 0) ptx::mbar_wait(&c.d_full[k], (u - 1) & 1, &c.abort);
-    }
-    if (sigma > 0) ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort);
-  }
-  if (warp >= 8 && warp < kMmaWarp) {
-    ptx::cp_async_wait_all();
-    if (threadIdx.x == kCopyBase && sigma > 0)
-      ptx::mbar_wait(&c.q_full, (sigma - 1) & 1, &c.abort);
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -655,6 +704,12 @@ cudaError_t prepare_device(int dev) {
   cudaError_t e = cudaFuncSetAttribute(choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        208 * 1024);
   if (e != cudaSuccess) return e;
+  // the register split assumes exactly kLaunchRegs a thread at launch: with fewer the
+  // scoring warpgroups' increase could never be granted
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, score_kernel);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
   e = cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)kScoreSmem);
   if (e != cudaSuccess) return e;

@@ -168,6 +168,11 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// Prefetch of the line that holds one address into L2.
+__device__ __forceinline__ void prefetch_line_l2(const void* src) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
+}
+
 // Arrive on `bar` once all of this thread's earlier cp.async copies landed
 // (without raising the barrier's expected count).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
