@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   __shared__ topk::Ctl c;
   __shared__ float hmax[64];
   topk::cg::cluster_group cl = topk::cg::this_cluster();
+  ptx::launch_dependents();
   const int r = blockIdx.y, b = r / p.q_len;
   int nb;
   const int n = rows_of(p, r, &nb);
@@ -886,6 +887,9 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
   // With fewer chosen blocks than CTAs a CTA takes two of them, down to sixteen
   // pieces a query: half the pieces to combine (one request of 64 blocks: 79 us
   // with 64 pieces, 74 with 32, 76 with 16; the workspace has room for more).
+  // With more, a whole number of CTAs a query, if that leaves few SMs out: no CTA
+  // then starts a second query (64 queries of 32 blocks: 116 us on 128 CTAs, 121 on
+  // 148).
   int splits = num_splits;
   if (splits == 0) {
     int sms = 0;
@@ -894,6 +898,7 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
     const long long tiles = (long long)rows * block_topk;
     splits = (int)std::min<long long>(
         sms, std::max<long long>((long long)rows * std::min(block_topk, 16), (tiles + 1) / 2));
+    if (splits == sms && rows <= sms && (sms - sms % rows) * 7 >= sms * 6) splits = sms - sms % rows;
   }
   p.out_blocks = out_blocks;
   p.out_table = reinterpret_cast<int*>(sel + layout(rows, num_heads, block_table_stride).total);

@@ -129,9 +129,12 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
   for (int b = tid; b < kPasses * kBins; b += kThreads) (&c.hist[0][0])[b] = 0;
   __syncthreads();
   uint32_t prefix = 0, mask = 0;
-  int left = want;
+  int left = want, pass = 0;
+  // once all keys of the chosen digit are taken the lower digits do not matter
+  // (distinct keys: two or three passes of the four)
+  bool all = false;
 #pragma unroll
-  for (int pass = 0; pass < kPasses; ++pass) {
+  for (; pass < kPasses && !all; ++pass) {
     const int shift = 24 - 8 * pass;
     uint32_t* h = c.hist[pass];
     rounds([&](int, uint32_t k, bool in) {
@@ -178,10 +181,10 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
     left -= c.above;
     prefix |= (uint32_t)c.digit << shift;
     mask |= 255u << shift;
+    all = left == c.equal;
   }
-  // The last pass's histogram counts the keys equal to T.  Their order matters
-  // only if some of them are left out.
-  const bool all = left == c.equal;
+  // Unless all are taken, the last pass's histogram counts the keys equal to T and
+  // their order decides.
   int seen = 0;
   if (!all) {
     if (tid == 0) c.share[0] = (int)c.hist[kPasses - 1][c.digit];
@@ -228,13 +231,18 @@ __device__ __forceinline__ void emit(Ctl& c, int lo, int hi, int (&base)[kLists]
                                      F&& f) {
   const int words = (hi - lo + 31) / 32, lane = threadIdx.x & 31;
   for (int w0 = 0; w0 < words; w0 += kThreads) {
+    // a batch's counts fit 16 bits each: one scan for both lists
+    static_assert(kLists <= 2 && 32 * kThreads < (1 << 15), "packed counts");
     const int w = w0 + threadIdx.x;
+    int n = 0, tot;
+    if (w < words)
+#pragma unroll
+      for (int l = 0; l < kLists; ++l) n += __popc(word(l, w)) << (16 * l);
+    const int ex = block_exclusive_scan(n, c.warp_sums, &tot);
 #pragma unroll
     for (int l = 0; l < kLists; ++l) {
-      int tot;
-      const int ex = block_exclusive_scan(w < words ? __popc(word(l, w)) : 0, c.warp_sums, &tot);
-      c.offs[l][threadIdx.x] = base[l] + ex;
-      base[l] += tot;
+      c.offs[l][threadIdx.x] = base[l] + ((ex >> (16 * l)) & 0xFFFF);
+      base[l] += (tot >> (16 * l)) & 0xFFFF;
     }
     __syncthreads();
     for (int k = threadIdx.x >> 5; k < kThreads && w0 + k < words; k += kThreads / 32)
