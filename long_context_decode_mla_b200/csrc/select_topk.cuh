@@ -68,19 +68,6 @@ __device__ __forceinline__ int before(cg::cluster_group& cl, Ctl& c, int which) 
   return s;
 }
 
-// Adds one to h[d] for every lane with `in`; a warp whose counted lanes agree
-// (keys of like size share their leading digits) adds once.
-__device__ __forceinline__ void count(uint32_t* h, bool in, uint32_t d) {
-  const uint32_t act = __ballot_sync(0xffffffffu, in);
-  if (!act) return;
-  const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(act) - 1);
-  if (__all_sync(0xffffffffu, !in || d == d0)) {
-    if ((threadIdx.x & 31) == 0) atomicAdd(&h[d0], (uint32_t)__popc(act));
-  } else if (in) {
-    atomicAdd(&h[d], 1u);
-  }
-}
-
 // mark() for slices whose keys are read again in every pass (kPer 0), or of at
 // most kPer keys a thread, held in registers.  key(i, first): `first` says that
 // the index is looked at for the first time.
@@ -137,8 +124,9 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
   for (; pass < kPasses && !all; ++pass) {
     const int shift = 24 - 8 * pass;
     uint32_t* h = c.hist[pass];
+    // plain increments without a result: the hardware merges a warp's equal digits
     rounds([&](int, uint32_t k, bool in) {
-      count(h, in && (k & mask) == prefix, (k >> shift) & 255u);
+      if (in && (k & mask) == prefix) atomicAdd(&h[(k >> shift) & 255u], 1u);
     });
     sync(cl);
     if (cl.num_blocks() > 1) {
@@ -191,18 +179,44 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
     sync(cl);
     seen = before(cl, c, 0);
   }
-  rounds([&](int i, uint32_t k, bool in) {
-    bool take = in && (all ? k >= prefix : k > prefix);
-    if (!all) {
-      const bool eq = in && k == prefix;
+  if (all) {
+    rounds([&](int i, uint32_t k, bool in) {
+      const uint32_t word = __ballot_sync(0xffffffffu, in && k >= prefix);
+      if (lane == 0 && in) bits[(i - lo) >> 5] = word;
+    });
+  } else {
+    // first the keys above T and, beside them, those equal to it; then the equal
+    // ones up to the `left`-th, a batch of words at a time
+    rounds([&](int i, uint32_t k, bool in) {
+      const uint32_t word = __ballot_sync(0xffffffffu, in && k > prefix);
+      const uint32_t same = __ballot_sync(0xffffffffu, in && k == prefix);
+      if (lane == 0 && in) {
+        bits[(i - lo) >> 5] = word;
+        if constexpr (kPer > 0) c.offs[0][(i - lo) >> 5] = (int)same;   // all in one batch
+      }
+    });
+    const int words = (hi - lo + 31) / 32;
+    static_assert(kPer * kThreads / 32 <= kThreads, "held keys make one batch of words");
+    for (int w0 = 0; w0 < words; w0 += kThreads) {
+      for (int j = tid >> 5; kPer == 0 && j < kThreads && w0 + j < words; j += kThreads / 32) {
+        const int i = lo + 32 * (w0 + j) + lane;
+        const uint32_t word = __ballot_sync(0xffffffffu, i < hi && key(i, false) == prefix);
+        if (lane == 0) c.offs[0][j] = (int)word;
+      }
+      __syncthreads();
+      const uint32_t eq = w0 + tid < words ? (uint32_t)c.offs[0][tid] : 0u;
       int tot;
-      const int rank = seen + block_exclusive_scan(eq ? 1 : 0, c.warp_sums, &tot);
+      const int before_w = seen + block_exclusive_scan(__popc(eq), c.warp_sums, &tot);
       seen += tot;
-      take = take || (eq && rank < left);
+      const int room = left - before_w;        // equal keys still taken in this word
+      if (eq && room > 0) {
+        uint32_t keep = eq;
+        for (int over = __popc(eq) - room; over > 0; --over) keep &= ~(0x80000000u >> __clz(keep));
+        bits[w0 + tid] |= keep;
+      }
+      __syncthreads();
     }
-    const uint32_t word = __ballot_sync(0xffffffffu, take);
-    if (lane == 0 && in) bits[(i - lo) >> 5] = word;
-  });
+  }
   sync(cl);      // `bits` complete; the shared fields may be written again
 }
 
@@ -216,6 +230,8 @@ __device__ __forceinline__ void mark(cg::cluster_group& cl, Ctl& c, int lo, int 
   const int n = hi - lo;
   if (n <= 2 * kThreads)
     mark_keys<2>(cl, c, lo, hi, want, bits, key);
+  else if (n <= 8 * kThreads)
+    mark_keys<8>(cl, c, lo, hi, want, bits, key);
   else if (n <= kHeld * kThreads)
     mark_keys<kHeld>(cl, c, lo, hi, want, bits, key);
   else
