@@ -358,16 +358,25 @@ def _kv(kv_dtype) -> int:
 
 
 def _nbytes(t) -> int:
-    return 0 if t is None else t.nbytes
-
-
-def _expect(name, t, dtype, shape=None):
-    """A tensor argument that is passed on as a raw pointer: its type, shape and order."""
     if t is None:
+        return 0
+    if not t.is_contiguous():
+        raise ValueError("a workspace must be contiguous")
+    return t.nbytes
+
+
+# The checks below run on every call of a serving step: plain comparisons first,
+# messages only once one has failed.
+
+def _expect(name, t, dtype, shape=None, numel=None):
+    """A tensor argument that is passed on as a raw pointer: its type, order and extent."""
+    if t is None or (t.dtype is dtype and t.is_contiguous()
+                     and (shape is None or t.shape == shape)
+                     and (numel is None or t.numel() == numel)):
         return
-    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        want = f"{dtype}" + ("" if shape is None else f" {list(shape)}")
-        raise ValueError(f"{name} must be contiguous {want}, got {t.dtype} {list(t.shape)}")
+    want = str(dtype) + ("" if shape is None else f" {list(shape)}") \
+        + ("" if numel is None else f" of {numel} values")
+    raise ValueError(f"{name} must be contiguous {want}, got {t.dtype} {list(t.shape)}")
 
 
 def _here(stream, *tensors) -> int:
@@ -394,18 +403,22 @@ def _at(t):
 
 def _query_shape(q) -> tuple[int, int, int]:
     """(batch, q_len, heads) of q [B, H, 576] or [B, q_len, H, 576]."""
-    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
-        raise ValueError(f"q must be [B, H, {HEAD_DIM}] or [B, q_len, H, {HEAD_DIM}], "
-                         f"got {list(q.shape)}")
+    s = q.shape
+    n = len(s)
+    if (n != 3 and n != 4) or s[-1] != HEAD_DIM:
+        raise ValueError(f"q must be [B, H, {HEAD_DIM}] or [B, q_len, H, {HEAD_DIM}], got {list(s)}")
     _expect("q", q, torch.bfloat16)
-    return (q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2])
+    return (s[0], s[1], s[2]) if n == 4 else (s[0], 1, s[1])
 
 
-def _expect_table(block_table, seq_lens, batch):
+def _expect_table(block_table, seq_lens, batch) -> int:
+    """The table's stride, for a table and lengths of `batch` requests."""
     _expect("seq_lens", seq_lens, torch.int32, (batch,))
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError(f"block_table must be [{batch}, stride], got {list(block_table.shape)}")
+    s = block_table.shape
+    if len(s) != 2 or s[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, stride], got {list(s)}")
     _expect("block_table", block_table, torch.int32)
+    return s[1]
 
 
 def _expect_cache(kv_cache, kv_dtype, num_blocks, block_size) -> int:
@@ -436,14 +449,15 @@ def mla_block_summary(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_s
     """
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
     kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
-    _expect_table(block_table, seq_lens, seq_lens.shape[0])
-    _expect("first_positions", first_positions, torch.int32, tuple(seq_lens.shape))
+    B = seq_lens.shape[0]
+    stride = _expect_table(block_table, seq_lens, B)
+    _expect("first_positions", first_positions, torch.int32, (B,))
     _expect("summaries", summaries, torch.uint8, (nb, SUMMARY_BYTES))
+    _expect("flags", flags, torch.int32)
     st = _here(stream, kv_cache, block_table, seq_lens, first_positions, summaries, flags)
     rc = lib().mla_block_summary(
-        _at(kv_cache), kvd, nb, block_size, _at(block_table), block_table.shape[1],
-        _at(seq_lens), _at(first_positions), block_table.shape[0], shard_id, num_shards,
-        _at(summaries), _at(flags), st)
+        _at(kv_cache), kvd, nb, block_size, _at(block_table), stride, _at(seq_lens),
+        _at(first_positions), B, shard_id, num_shards, _at(summaries), _at(flags), st)
     _check(rc, "mla_block_summary")
 
 
@@ -462,18 +476,16 @@ def mla_block_select(q, summaries, block_table, seq_lens, shard_id, num_shards, 
     with [B, q_len] in front).
     """
     B, Q, H = _query_shape(q)
-    _expect_table(block_table, seq_lens, B)
+    stride = _expect_table(block_table, seq_lens, B)
     _expect("summaries", summaries, torch.uint8, (summaries.shape[0], SUMMARY_BYTES))
     for name, t, n in (("out_table", out_table, B * Q * block_topk), ("out_lens", out_lens, B * Q),
                        ("out_blocks", out_blocks, B * Q * block_topk)):
-        _expect(name, t, torch.int32)
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name} must hold {n} values, got {list(t.shape)}")
+        _expect(name, t, torch.int32, None, n)
     st = _here(stream, q, summaries, block_table, seq_lens, out_table, out_lens, out_blocks,
                workspace)
     rc = lib().mla_block_select(
         _at(q), _at(summaries), summaries.shape[0], block_size, _at(block_table),
-        block_table.shape[1], _at(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
+        stride, _at(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
         sink_blocks, recent_blocks, _at(out_blocks), _at(out_table), _at(out_lens),
         _at(workspace), _nbytes(workspace), st)
     _check(rc, "mla_block_select")
@@ -496,20 +508,18 @@ def mla_decode_blocks(q, kv_cache, kv_dtype, summaries, block_table, seq_lens, s
     B, Q, H = _query_shape(q)
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
     kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
-    _expect_table(block_table, seq_lens, B)
+    stride = _expect_table(block_table, seq_lens, B)
     _expect("summaries", summaries, torch.uint8, (nb, SUMMARY_BYTES))
     for name, t, dtype, n in (("out_partial", out_partial, torch.float32, B * Q * H * V_DIM),
                               ("out_lse", out_lse, torch.float32, B * Q * H),
                               ("out_blocks", out_blocks, torch.int32, B * Q * block_topk)):
-        _expect(name, t, dtype)
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name} must hold {n} values, got {list(t.shape)}")
+        _expect(name, t, dtype, None, n)
     impl_code = IMPLS[impl] if isinstance(impl, str) else int(impl)
     st = _here(stream, q, kv_cache, summaries, block_table, seq_lens, out_partial, out_lse,
                out_blocks, workspace)
     rc = lib().mla_decode_blocks(
         _at(q), _at(kv_cache), kvd, _at(summaries), nb, block_size, _at(block_table),
-        block_table.shape[1], _at(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
+        stride, _at(seq_lens), B, H, Q, shard_id, num_shards, block_topk,
         sink_blocks, recent_blocks, float(softmax_scale), _at(out_partial), _at(out_lse),
         _at(out_blocks), _at(workspace), _nbytes(workspace), num_splits, impl_code,
         st)
@@ -530,15 +540,13 @@ def mla_attention_mass(q, kv_cache, kv_dtype, block_table, seq_lens, shard_id, n
     B, Q, H = _query_shape(q)
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
     kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
-    _expect_table(block_table, seq_lens, B)
-    _expect("lse", lse, torch.float32)
-    if lse.numel() != B * Q * H:
-        raise ValueError(f"lse must hold {B * Q * H} values, got {list(lse.shape)}")
+    stride = _expect_table(block_table, seq_lens, B)
+    _expect("lse", lse, torch.float32, None, B * Q * H)
     _expect("mass", mass, torch.float32, (B, mass.shape[-1]))
     st = _here(stream, q, kv_cache, block_table, seq_lens, lse, mass, workspace)
     rc = lib().mla_attention_mass(
         _at(q), _at(kv_cache), kvd, nb, block_size, _at(block_table),
-        block_table.shape[1], _at(seq_lens), B, H, Q, shard_id, num_shards, float(softmax_scale),
+        stride, _at(seq_lens), B, H, Q, shard_id, num_shards, float(softmax_scale),
         _at(lse), float(decay), _at(mass), mass.shape[-1], _at(workspace), _nbytes(workspace),
         num_splits, st)
     _check(rc, "mla_attention_mass")
@@ -558,7 +566,7 @@ def mla_cache_evict(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_sha
     B = seq_lens.shape[0]
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
     kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
-    _expect_table(block_table, seq_lens, B)
+    stride = _expect_table(block_table, seq_lens, B)
     shape = (B, mass.shape[-1])
     for name, t, dtype, sh in (("mass", mass, torch.float32, shape),
                                ("mass_out", mass_out, torch.float32, shape),
@@ -570,7 +578,7 @@ def mla_cache_evict(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_sha
     st = _here(stream, kv_cache, block_table, seq_lens, rows, mass, positions, mass_out,
                positions_out, rows_out, workspace)
     rc = lib().mla_cache_evict(
-        _at(kv_cache), kvd, nb, block_size, _at(block_table), block_table.shape[1],
+        _at(kv_cache), kvd, nb, block_size, _at(block_table), stride,
         _at(seq_lens), _at(rows), B, shard_id, num_shards, _at(mass), _at(positions),
         mass.shape[-1], budget, sink, recent, _at(mass_out), _at(positions_out), _at(rows_out),
         _at(workspace), _nbytes(workspace), st)
