@@ -19,7 +19,10 @@
 //    decode kernel's operand image (two e4m3 terms in one power-of-two frame,
 //    q_image.cuh).  Every 128-value scale group is a part with an accumulator of
 //    its own, scaled in fp32, and the bf16 rope a fifth.
-//  * bf16 rows and queries multiply as they are (exact products), in one part.
+//  * bf16 rows and queries multiply as they are (exact products), in three parts
+//    of 192 values that are added in fp32: the tensor core cuts low bits at each
+//    of its additions, and 36 in one accumulator left 2.3e-6 of the weights'
+//    error against 0.6e-6 so.
 //
 // A tile is two cache blocks (M = 128: a weight-stationary M = 64 MMA takes as
 // long, and 36 of them more than a block's share of HBM time).  Its rows go
@@ -78,8 +81,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <int kDtype>
 struct Shape;
 // kMeta tiles can be between their load and their weights at once: eight slots
-// and eight accumulators hold 3.2 fp8 tiles of five parts, or 0.9 and 8 bf16
-// tiles (accumulated in one part).
+// and eight accumulators hold 1.6 and 1.6 fp8 tiles, 0.9 and 2.7 bf16 tiles.
 template <>
 struct Shape<kKvFp8> {
   static constexpr int kRowBytes = kRowBytesFp8, kChunks = 5, kParts = 5, kMeta = 4,
@@ -87,7 +89,7 @@ struct Shape<kKvFp8> {
 };
 template <>
 struct Shape<kKvBf16> {
-  static constexpr int kRowBytes = kRowBytesBf16, kChunks = 9, kParts = 1, kMeta = 10,
+  static constexpr int kRowBytes = kRowBytesBf16, kChunks = 9, kParts = 3, kMeta = 10,
                        kIssuers = 1;
 };
 constexpr int kMaxMeta = 10;
@@ -246,8 +248,8 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
 // D = K Q^T (M = 128 rows, N = 64 heads, 64 TMEM columns a part).  A wait
 // costs an issuing thread some 600 cycles while the tensor core streams its
 // operands, as much as eight MMAs take: fp8 parts alternate between two issuers
-// (77 cycles an MMA, 36 a tile), and bf16, whose chunks accumulate in one part
-// and so keep to one thread, waits for three chunks at a time.
+// (77 cycles an MMA, 36 a tile); one is enough for bf16 rows, whose tile has
+// twice the time, and waits for a part's three chunks at once.
 template <int kDtype>
 __device__ __forceinline__ void mma_role(const MassParams& m, Ctl& c, uint8_t* base, int nseg,
                                          uint32_t side, Counts& n) {
@@ -292,31 +294,34 @@ __device__ __forceinline__ void mma_role(const MassParams& m, Ctl& c, uint8_t* b
         ptx::mma_commit(&c.d_full[buf]);
       }
     } else {
-      const uint32_t buf = n.part % kBufs;
-      if (n.part >= (uint32_t)kBufs &&
-          !ptx::mbar_wait(&c.d_empty[buf], ((n.part / kBufs) + 1) & 1, &c.abort))
-        return;
-      const uint32_t d = c.tmem_base + 64 * buf;
 #pragma unroll 1
-      for (int k3 = 0; k3 < S::kChunks; k3 += 3) {
-        const uint32_t c0 = n.chunk, c1 = c0 + 1, c2 = c0 + 2;
-        if (!ptx::mbar_wait3(&c.full[c0 % kSlots], (c0 / kSlots) & 1, &c.full[c1 % kSlots],
-                             (c1 / kSlots) & 1, &c.full[c2 % kSlots], (c2 / kSlots) & 1, &c.abort))
-          return;
+      for (int j = 0; j < S::kParts; ++j, ++n.part) {
+        const uint32_t buf = n.part % kBufs;
+        const bool reuse = n.part >= (uint32_t)kBufs;
+        uint64_t* bars[4];
+        uint32_t pars[4];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          bars[i] = &c.full[(n.chunk + i) % kSlots];
+          pars[i] = ((n.chunk + i) / kSlots) & 1;
+        }
+        bars[3] = reuse ? &c.d_empty[buf] : bars[0];
+        pars[3] = reuse ? ((n.part / kBufs) + 1) & 1 : pars[0];
+        if (!ptx::mbar_wait4(bars, pars, &c.abort)) return;
         ptx::tc_fence_after();
+        const uint32_t d = c.tmem_base + 64 * buf;
 #pragma unroll 1
-        for (int k = k3; k < k3 + 3; ++k, ++n.chunk) {
+        for (int i = 0; i < 3; ++i, ++n.chunk) {
           const uint32_t s = n.chunk % kSlots;
           const uint64_t dk = dplus(dk0, s * kSlot);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            ptx::mma_f16(d, dplus(dk, ks * 32), dplus(dq, k * kHalf + ks * 32), kIdBf,
-                         (k | ks) != 0);
+            ptx::mma_f16(d, dplus(dk, ks * 32), dplus(dq, (3 * j + i) * kHalf + ks * 32), kIdBf,
+                         (i | ks) != 0);
           ptx::mma_commit(&c.empty[s]);
         }
+        ptx::mma_commit(&c.d_full[buf]);
       }
-      ptx::mma_commit(&c.d_full[buf]);
-      ++n.part;
     }
     if (cur.last_of_segment()) ptx::mma_commit(&c.q_empty);
     ++n.tau;
@@ -397,14 +402,18 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
       if (k < S::kParts - 1) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          v[e] = k == 0 ? sc[0] * __uint_as_float(x[e]) : fmaf(sc[k & 3], __uint_as_float(x[e]), v[e]);
+          if constexpr (kDtype == kKvFp8)
+            v[e] = k == 0 ? sc[0] * __uint_as_float(x[e])
+                          : fmaf(sc[k & 3], __uint_as_float(x[e]), v[e]);
+          else
+            v[e] = k == 0 ? __uint_as_float(x[e]) : v[e] + __uint_as_float(x[e]);
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float2 f = c.head[32 * hh + e];
-          const float y = S::kParts > 1
-                              ? fmaf(f.x, v[e], fmaf(sl2, __uint_as_float(x[e]), -f.y))
-                              : fmaf(f.x, __uint_as_float(x[e]), -f.y);
+          const float z = __uint_as_float(x[e]);       // the rope (fp8), the last third
+          const float y = kDtype == kKvFp8 ? fmaf(f.x, v[e], fmaf(sl2, z, -f.y))
+                                           : fmaf(f.x, v[e] + z, -f.y);
           float w = ex2(y);
           if (masked && 32 * hh + e < from) w = 0.f;
           sum += w;
