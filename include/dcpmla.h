@@ -484,8 +484,8 @@ int pcp_prefill_attention(const void* q, const int32_t* positions, int num_queri
  *   flags            NULL or a DEVICE int32: DCPMLA_FLAG_BAD_BLOCK,
  *                    DCPMLA_FLAG_BAD_LENGTH; such blocks are skipped.
  * Rows past a request's end do not enter the mean, whatever they hold.  A block
- * that several requests share should be full or of one length in all of them:
- * else its summary is that of any one of them.
+ * that several requests share has to hold the same rows for all of them (a
+ * common prefix of whole blocks does): else its summary is undefined.
  * Returns DCPMLA_OK or a negative code.
  */
 #define DCPMLA_SUMMARY_BYTES 608
@@ -505,7 +505,8 @@ int mla_block_summary(const void* kv_cache, int kv_dtype, int64_t num_blocks, in
  * in fp32, each operation rounded by itself.  Taken are the first sink_blocks
  * and the last recent_blocks of the request's blocks on this shard, then the
  * highest ranks, ties to the lowest index, block_topk in all (all of them if
- * there are no more).  The choice does not depend on launch shapes.
+ * there are no more).  The choice does not depend on launch shapes.  A summary
+ * counts all rows of its block; what a query reads of it ends with what it sees.
  *
  *   q           [batch][q_len][num_heads][576] bf16, 16-byte aligned; query i
  *               of request b sees the positions up to L_b - q_len + i.  num_heads
@@ -608,7 +609,7 @@ int mla_attention_mass(const void* q, const void* kv_cache, int kv_dtype, int64_
  *   mass_out, positions_out  the kept rows' entries in their new order, the rest
  *                 untouched; each may be the input array itself (no other
  *                 overlap).  positions_out may be NULL.
- *   rows_out      [batch] int32, not `rows`.
+ *   rows_out      [batch] int32, not `rows` nor `seq_lens`.
  *   kv_cache      rows are moved within each request's blocks: no block written
  *                 to may be shared with another request.
  *   workspace     mla_cache_evict_workspace_size(...) bytes, 16-byte aligned; its

@@ -226,7 +226,8 @@ int mla_cache_evict(void* kv_cache, int kv_dtype, int64_t num_blocks, int block_
       std::min<long long>((long long)block_table_stride * kBlock, mass_stride) > kMaxRows)
     return DCPMLA_ERR_UNSUPPORTED;
   if (batch == 0) return DCPMLA_OK;
-  if (!kv_cache || !block_table || !seq_lens || !mass || !mass_out || !rows_out || rows_out == rows)
+  if (!kv_cache || !block_table || !seq_lens || !mass || !mass_out || !rows_out ||
+      rows_out == rows || rows_out == seq_lens)
     return DCPMLA_ERR_INVALID_ARGUMENT;
   if (!aligned16(kv_cache) || (workspace && !aligned16(workspace))) return DCPMLA_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < evict_bytes(batch, budget)) return DCPMLA_ERR_WORKSPACE;

@@ -61,7 +61,7 @@ __device__ __forceinline__ int units_of(const SummaryParams& p, int b, int* firs
   bool bad = L < 0;
   if (bad) L = 0;
   int n = local_len(L, p.shard, p.nshards);
-  int nb = (n - 1 + kBlock) / kBlock;
+  int nb = n > 0 ? (n - 1) / kBlock + 1 : 0;
   if (nb > p.bt_stride) {
     bad = true;
     nb = p.bt_stride;

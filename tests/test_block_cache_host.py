@@ -24,7 +24,7 @@ DECODE = dict(q=P, kv=P, dtype=1, s=P, nb=10, bs=64, table=P, stride=4, lens=P, 
 MASS = dict(q=P, kv=P, dtype=1, nb=10, bs=64, table=P, stride=4, lens=P, batch=2, heads=8, q_len=1, shard=0, n=1,
             scale=0.1, lse=P, decay=1.0, mass=P, mstride=256, ws=P, wsb=BIG, splits=4, stream=None)
 EVICT = dict(kv=P, dtype=1, nb=10, bs=64, table=P, stride=4, lens=P, rows=None, batch=2, shard=0, n=1, mass=P, pos=None,
-             mstride=256, budget=100, sink=1, recent=9, mo=P, po=None, ro=P, ws=P, wsb=BIG, stream=None)
+             mstride=256, budget=100, sink=1, recent=9, mo=P, po=None, ro=2 * P, ws=P, wsb=BIG, stream=None)
 CALLS = {"mla_block_summary": SUMMARY, "mla_block_select": SELECT, "mla_decode_blocks": DECODE,
          "mla_attention_mass": MASS, "mla_cache_evict": EVICT}
 
@@ -58,7 +58,8 @@ REFUSED = {
         (dict(lse=None), EINVAL), (dict(mass=None), EINVAL), (dict(mstride=0), EINVAL), (dict(decay=-0.5), EINVAL),
         (dict(decay=float("nan")), EINVAL)],
     "mla_cache_evict": SHARED + CACHE + WORK + [
-        (dict(mass=None), EINVAL), (dict(mo=None), EINVAL), (dict(ro=None), EINVAL), (dict(rows=P), EINVAL),
+        (dict(mass=None), EINVAL), (dict(mo=None), EINVAL), (dict(ro=None), EINVAL), (dict(rows=2 * P), EINVAL),
+        (dict(lens=P + 16, ro=P + 16), EINVAL),
         (dict(budget=0), EINVAL), (dict(sink=-1), EINVAL), (dict(recent=-1), EINVAL),
         (dict(sink=50, recent=51), EINVAL), (dict(mstride=0), EINVAL), (dict(batch=70000), EUNSUP),
         (dict(stride=1 << 20, mstride=1 << 26), EUNSUP)],
