@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
     keys[k - lo] = p.keys ? __ldcg(p.keys + (size_t)r * p.bt_stride + k) : rank_key(p, hmax, r, k, nb);
   __syncthreads();
   if (want > 0)
-    topk::mark(cl, c, lo, hi, want, bits, [&](int i, bool) { return keys[i - lo]; });
+    topk::mark(cl, c, lo, hi, want, bits, [&](int i) { return keys[i - lo]; },
+               [](int, uint32_t k, bool) { return k; });
   // places of this slice's blocks in the list
   int pos[1] = {0};
   if (cl.num_blocks() > 1) {

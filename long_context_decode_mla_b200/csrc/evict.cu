@@ -97,16 +97,20 @@ __global__ void __launch_bounds__(topk::kThreads) pick_kernel(const EvictParams 
   const int fresh = L - p.recent;    // positions from here on are recent
   const bool put_mass = p.mass_out != p.mass;
   const bool put_pos = p.positions_out && p.positions_out != p.positions;
-  topk::mark(cl, c, lo, hi, keep, bits, [&](int j, bool first) {
-    const int t = position_of(p, base, j);
-    const float m = p.mass[base + j];
-    if (first && j < p.budget) {
-      // as if the row stayed; the move kernel corrects the freed places
-      if (put_mass) p.mass_out[base + j] = m;
-      if (put_pos) p.positions_out[base + j] = t;
-    }
-    return t < p.sink || t >= fresh ? 0xFFFFFFFFu : topk::key_of(m);
-  });
+  struct Row {
+    float mass;
+    int position;
+  };
+  topk::mark(
+      cl, c, lo, hi, keep, bits, [&](int j) { return Row{p.mass[base + j], position_of(p, base, j)}; },
+      [&](int j, const Row& row, bool first) {
+        if (first && j < p.budget) {
+          // as if the row stayed; the move kernel corrects the freed places
+          if (put_mass) p.mass_out[base + j] = row.mass;
+          if (put_pos) p.positions_out[base + j] = row.position;
+        }
+        return row.position < p.sink || row.position >= fresh ? 0xFFFFFFFFu : topk::key_of(row.mass);
+      });
   // Freed places (below the budget, not taken) and moving rows (taken, at or
   // past it) of this slice; every mass has been read by now.
   auto word = [&](int list, int w) {

@@ -32,8 +32,8 @@ constexpr int kMaxCluster = 8;   // the largest portable cluster
 constexpr int kPasses = 4;
 
 struct Ctl {
-  uint32_t hist[kPasses][kBins];   // this CTA's digit counts
-  uint32_t total[kBins];           // the cluster's, of the current pass
+  alignas(16) uint32_t hist[kPasses][kBins];   // this CTA's digit counts
+  alignas(16) uint32_t total[kBins];           // the cluster's, of the current pass
   int warp_sums[kThreads / 32];
   int digit, above, equal;         // chosen digit, keys above it and in it (whole cluster)
   int share[2];                    // what the other CTAs of the cluster read of this one
@@ -63,25 +63,31 @@ __device__ __forceinline__ void sync(cg::cluster_group& cl) {
 // Sum of `share[which]` over the CTAs before this one (call between cluster
 // barriers that order the writes and the next reuse).
 __device__ __forceinline__ int before(cg::cluster_group& cl, Ctl& c, int which) {
-  int s = 0;
-  for (unsigned r = 0; r < cl.block_rank(); ++r) s += cl.map_shared_rank(c.share, r)[which];
-  return s;
+  const unsigned r = threadIdx.x & 31;        // a lane a CTA: the reads are in flight together
+  const int v = r < cl.block_rank() ? cl.map_shared_rank(c.share, r)[which] : 0;
+  return (int)__reduce_add_sync(0xffffffffu, (unsigned)v);
 }
 
 // mark() for slices whose keys are read again in every pass (kPer 0), or of at
-// most kPer keys a thread, held in registers.  key(i, first): `first` says that
-// the index is looked at for the first time.
-template <int kPer, class KeyFn>
+// most kPer keys a thread, held in registers.
+template <int kPer, class LoadFn, class KeyFn>
 __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo, int hi, int want,
-                                          uint32_t* bits, KeyFn&& key) {
+                                          uint32_t* bits, LoadFn&& load, KeyFn&& key) {
+  using Raw = decltype(load(0));
   const int tid = threadIdx.x, lane = tid & 31;
   constexpr int kRegs = kPer > 0 ? kPer : 1;
   uint32_t held[kRegs];
   if constexpr (kPer > 0) {
+    Raw raw[kRegs];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = lo + j * kThreads + tid;
-      held[j] = i < hi ? key(i, true) : 0u;
+      if (i < hi) raw[j] = load(i);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = lo + j * kThreads + tid;
+      held[j] = i < hi ? key(i, raw[j], true) : 0u;
     }
   }
   // f(index, key, inside) for this thread's keys, in rounds of kThreads; all
@@ -98,10 +104,16 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
     } else {
       for (int base = lo; base < hi; base += 8 * kThreads) {
         uint32_t k[8];
+        Raw raw[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int i = base + j * kThreads + tid;
-          k[j] = i < hi ? key(i, first) : 0u;
+          if (i < hi) raw[j] = load(i);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = base + j * kThreads + tid;
+          k[j] = i < hi ? key(i, raw[j], first) : 0u;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -130,12 +142,21 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
     });
     sync(cl);
     if (cl.num_blocks() > 1) {
-      if (tid < kBins) {
-        uint32_t s = 0;
+      if (tid < kBins / 4) {
+        uint4 v[kMaxCluster];
+        uint4 s = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (unsigned r = 0; r < (unsigned)kMaxCluster; ++r)
-          if (r < cl.num_blocks()) s += cl.map_shared_rank(h, r)[tid];
-        c.total[tid] = s;
+          v[r] = r < cl.num_blocks() ? reinterpret_cast<const uint4*>(cl.map_shared_rank(h, r))[tid]
+                                     : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          s.x += v[r].x;
+          s.y += v[r].y;
+          s.z += v[r].z;
+          s.w += v[r].w;
+        }
+        reinterpret_cast<uint4*>(c.total)[tid] = s;
       }
       __syncthreads();
       h = c.total;
@@ -200,7 +221,7 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
     for (int w0 = 0; w0 < words; w0 += kThreads) {
       for (int j = tid >> 5; kPer == 0 && j < kThreads && w0 + j < words; j += kThreads / 32) {
         const int i = lo + 32 * (w0 + j) + lane;
-        const uint32_t word = __ballot_sync(0xffffffffu, i < hi && key(i, false) == prefix);
+        const uint32_t word = __ballot_sync(0xffffffffu, i < hi && key(i, load(i), false) == prefix);
         if (lane == 0) c.offs[0][j] = (int)word;
       }
       __syncthreads();
@@ -221,21 +242,22 @@ __device__ __forceinline__ void mark_keys(cg::cluster_group& cl, Ctl& c, int lo,
 }
 
 // Marks the taken indices of this CTA's slice [lo, hi) in `bits` (bit i - lo;
-// room for ceil((hi - lo) / 32) words).  key(i, first) is called for every index
-// of the slice, with `first` once and possibly again without.  All threads of all CTAs of the cluster call
+// room for ceil((hi - lo) / 32) words).  load(i) reads what the key of index i is
+// made of, key(i, raw, first) makes it: for every index with `first` once, possibly
+// again without.  A thread's loads come before its key() calls, which may write.  All threads of all CTAs of the cluster call
 // it with the same n and 1 <= want <= n.
-template <class KeyFn>
+template <class LoadFn, class KeyFn>
 __device__ __forceinline__ void mark(cg::cluster_group& cl, Ctl& c, int lo, int hi, int want,
-                                     uint32_t* bits, KeyFn&& key) {
+                                     uint32_t* bits, LoadFn&& load, KeyFn&& key) {
   const int n = hi - lo;
   if (n <= 2 * kThreads)
-    mark_keys<2>(cl, c, lo, hi, want, bits, key);
+    mark_keys<2>(cl, c, lo, hi, want, bits, load, key);
   else if (n <= 8 * kThreads)
-    mark_keys<8>(cl, c, lo, hi, want, bits, key);
+    mark_keys<8>(cl, c, lo, hi, want, bits, load, key);
   else if (n <= kHeld * kThreads)
-    mark_keys<kHeld>(cl, c, lo, hi, want, bits, key);
+    mark_keys<kHeld>(cl, c, lo, hi, want, bits, load, key);
   else
-    mark_keys<0>(cl, c, lo, hi, want, bits, key);
+    mark_keys<0>(cl, c, lo, hi, want, bits, load, key);
 }
 
 // Numbers the set bits of kLists masks of the slice in index order:
