@@ -70,10 +70,7 @@ constexpr int kSlots = 8;
 constexpr int kBufs = 8;                           // TMEM accumulators of 64 columns
 constexpr uint32_t kTmemCols = 64 * kBufs;
 constexpr uint32_t kQBytes = 9 * kHalf;            // fp8: hi, lo, rope; bf16: nine chunks
-#ifndef KPF
-#define KPF 1
-#endif
-constexpr int kPrefetchTiles = KPF;
+constexpr int kPrefetchTiles = 1;                  // more crowd the L2: 61 us at 1, 86 at 4
 constexpr int kMaxSeg = 64;
 constexpr int kTileMass = 128;                     // rows of a tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -187,7 +184,10 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
       }
     pf_ok = pf.next(p, c);
   };
-  for (int i = 0; i < kPrefetchTiles; ++i) prefetch();
+  // the first tile's own loads come before any prefetch: its table entries and
+  // the prefetch instructions would hold them up by 2,000 cycles
+  int ahead = kPrefetchTiles;
+  pf_ok = pf.next(p, c);
   while (true) {
     // a bad table entry: a stand-in block, no rows; a missing second block: nothing
     int blk[2], halves = 1;
@@ -240,7 +240,8 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
       }
     }
     ++n.tau;
-    prefetch();
+    for (; ahead > 0; --ahead) prefetch();
+    ahead = 1;
     if (!cur.next(p, c)) break;
   }
 }

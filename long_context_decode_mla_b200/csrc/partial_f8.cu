@@ -274,13 +274,11 @@ __device__ __forceinline__ void producer_role(const F8Params& P, const PartialPa
   const bool lead = lane == 0;
   TileCursor cur, pf;
   if (!cur.start(p, c, nseg)) return;
+  // L2 prefetch, kPrefetchTiles ahead of the loads.  The first tile's own loads
+  // come before the first burst, which would hold them up by 2,000 cycles.
   pf = cur;
-  bool pf_ok = !kListed;
-  for (int i = 0; i < kPrefetchTiles && pf_ok; ++i) {
-    const int blk = tile_block(p, pf.v.b, (pf.v.row_begin >> 6) + pf.t);
-    if (lead && blk >= 0) ptx::prefetch_l2(p.kv + (size_t)blk * kTileBytes, kTileBytes);
-    pf_ok = pf.next(p, c);
-  }
+  bool pf_ok = !kListed && pf.next(p, c);
+  int pf_due = kPrefetchTiles;
   while (true) {
     const uint32_t cs = tau % kCodeStages, rs = tau % kRopeStages;
     // slot reuse: the PV of tile tau - 3 and the rope part of tile tau - 2
@@ -337,11 +335,12 @@ __device__ __forceinline__ void producer_role(const F8Params& P, const PartialPa
     }
     ++tau;
     if (!cur.next(p, c)) break;
-    if (pf_ok) {
+    for (; pf_ok && pf_due > 0; --pf_due) {
       const int pb = tile_block(p, pf.v.b, (pf.v.row_begin >> 6) + pf.t);
       if (lead && pb >= 0) ptx::prefetch_l2(p.kv + (size_t)pb * kTileBytes, kTileBytes);
       pf_ok = pf.next(p, c);
     }
+    pf_due = 1;
   }
 }
 
