@@ -522,7 +522,9 @@ int mla_block_summary(const void* kv_cache, int kv_dtype, int64_t num_blocks, in
  *               (shard_id 0, num_shards 1).
  *   out_lens    [batch][q_len] int32: rows in the blocks taken.
  *   workspace   mla_block_select_workspace_size(...) bytes, 16-byte aligned;
- *               its flag word as in mla_decode_workspace_size.
+ *               its flag word as in mla_decode_workspace_size.  Calls that may
+ *               overlap on the device (other streams, other graphs) need a
+ *               workspace each; so with every call below.
  * A table entry outside the pool is flagged and ranks last.
  * Returns DCPMLA_OK or a negative code.
  */

@@ -304,18 +304,16 @@ inline int slice_words(long long n, int size) {
   return (int)(((n + size - 1) / size + 31) / 32);
 }
 
-// CTAs a cluster takes for rows of up to n keys.  A cluster's barriers cost
-// some 3 us over a block's (7 against 10 us at 8 keys, 14 against 17 at 2,112),
-// so one CTA works alone up to 4,096; past that as many as leave 2,048 keys each
-// while the clusters fit the device's waves (clusters of 8 for 64 rows: twice
-// the time of clusters of 4).
+// CTAs a cluster takes for rows of up to n keys.  A cluster's barriers cost 2 to
+// 3 us over a block's, so one CTA works alone up to 4,096 keys (one row of 1,024:
+// 4.2 us alone, 6.6 by two; of 4,096: 7.7 and 9.7); past that as many as leave
+// 2,048 keys each (16 rows of 16,384: 33.0, 14.9, 11.1 and 10.7 us by 1, 2, 4 and 8)
+// while the clusters fill the device no more than twice (64 rows of 16,384: 14.1 us
+// by 4, 22.8 by 8).
 inline int cluster_size(long long n, int rows, int sms) {
-#ifdef FORCE_SIZE
-  return FORCE_SIZE;
-#endif
   int size = 1;
   if (n <= 4096) return size;
-  while (size < kMaxCluster && n > 2048ll * size && 2ll * rows * size <= 2ll * sms) size *= 2;
+  while (size < kMaxCluster && n > 2048ll * size && (long long)rows * size <= sms) size *= 2;
   return size;
 }
 
