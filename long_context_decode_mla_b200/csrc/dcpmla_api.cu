@@ -267,7 +267,7 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
     p.request_aligned = 1;
     p.num_ctas = std::max(min_ctas, std::min(batch, ctas));
   }
-  enum { kSimt, kTc16, kTc8 } which;
+  enum { kSimt, kTc16, kTc8, kTcBf } which;
   if (impl == DCPMLA_IMPL_SIMT) {
     which = kSimt;
   } else if (impl == DCPMLA_IMPL_TC_F16) {
@@ -275,6 +275,8 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
     which = kTc16;
   } else if (f8_ok) {
     which = kTc8;
+  } else if (chosen && bf16_supports(p, kv_dtype)) {
+    which = kTcBf;
   } else if (tc_ok) {
     which = kTc16;
   } else if (impl == DCPMLA_IMPL_TC) {
@@ -285,6 +287,7 @@ int decode_partial(const void* q, const void* kv_cache, int kv_dtype, int64_t nu
   if (q_len > 1 && which == kSimt) return DCPMLA_ERR_UNSUPPORTED;   // causal rows: tensor cores only
 
   cudaError_t e = which == kTc8    ? launch_partial_f8(p, st)
+                  : which == kTcBf ? launch_partial_bf16(p, st)
                   : which == kTc16 ? launch_partial_tc(p, kv_dtype, st)
                                    : launch_partial_simt(p, kv_dtype, st);
   if (e != cudaSuccess) return DCPMLA_ERR_CUDA;

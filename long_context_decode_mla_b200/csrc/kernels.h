@@ -53,6 +53,8 @@ cudaError_t launch_partial_tc(const PartialParams& p, int kv_dtype, cudaStream_t
 bool tc_supports(const PartialParams& p, int kv_dtype);
 cudaError_t launch_partial_f8(const PartialParams& p, cudaStream_t st);
 bool f8_supports(const PartialParams& p, int kv_dtype);
+cudaError_t launch_partial_bf16(const PartialParams& p, cudaStream_t st);   // chosen blocks
+bool bf16_supports(const PartialParams& p, int kv_dtype);
 cudaError_t launch_split_combine(const PartialParams& p, cudaStream_t st);
 cudaError_t launch_dcp_merge(const float* partials, const float* lses, int num_shards, int batch,
                              int heads, float* out, float* out_lse, cudaStream_t st);
