@@ -469,8 +469,8 @@ int pcp_prefill_attention(const void* q, const int32_t* positions, int num_queri
  *
  * A summary is the mean of the block's rows (576 values, rope included) as
  * int8 codes, 608 bytes: 576 codes, 5 fp32 scales (latent groups of 128 values,
- * then the 64 rope values), 12 bytes of zeros.  Per group scale = max|mean| /
- * 127 (1 if that is 0), code = mean / scale rounded to nearest even; a mean
+ * then the 64 rope values), 12 bytes of zeros.  Per group scale = max|mean| *
+ * fp32(1/127) (1 if that is 0), code = mean / scale rounded to nearest even; a mean
  * that is not finite counts as 0.  The pages have no counterpart to this call.
  *
  *   summaries        [num_blocks][608], 16-byte aligned: the summary of cache
@@ -497,8 +497,8 @@ int mla_block_summary(const void* kv_cache, int kv_dtype, int64_t num_blocks, in
 /*
  * The blocks of this shard that each query token reads, by the summaries.
  *
- * Per head and group the query is held as int8 codes too (step = max|q| / 127,
- * 1 if that is 0; values that are not finite count as 0), and with the code
+ * Per head and group the query is held as int8 codes too (step = max|q| *
+ * fp32(1/127), 1 if that is 0; values that are not finite count as 0), and with the code
  * products dot_g (whole numbers)
  *     s_hb   = sum over groups, in order, of fp32(dot_g) * (step_hg * scale_bg)
  *     rank_b = max_h (s_hb - max_b' s_hb')

@@ -2,8 +2,8 @@
 // summaries (int8 codes of the mean key and their scales), and the decode over
 // the chosen blocks.
 //
-//   q codes: per head and scale group, step = max|q| / 127 (1 if 0), code =
-//            rint(q / step)                                 (values not finite: 0)
+//   q codes: per head and scale group, step = max|q| * fp32(1/127) (1 if 0), code
+//            = rint(q / step)                               (values not finite: 0)
 //   s_hb   = sum over the five groups, in order, of
 //            fp32(codes_q . codes_b) * (step_hg * scale_bg)  (fp32, no fusing)
 //   rank_b = max_h (s_hb - max_b' s_hb')
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParam
   }
   finite = __reduce_max_sync(0xffffffffu, finite);
   const float amax = __uint_as_float(finite);
-  const float step = amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
+  const float up = __fmul_rn(amax, kInv127), step = up > 0.f ? up : 1.f;
   uint32_t code = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {

@@ -26,6 +26,7 @@ constexpr int kRowBytesFp8 = 656;
 constexpr int kQImageBytes = 2 * 4 * 8192 + 8192 + 64 * 4;
 // Summary of one cache block: 576 int8 codes, 5 fp32 scales, 12 bytes of zeros.
 constexpr int kSummaryBytes = 608;
+constexpr float kInv127 = 1.f / 127.f;   // int8 steps are largest magnitude * this, one rounding
 constexpr int kWsHeader = 256;    // workspace header: flag word + reserved
 constexpr int kMaxDevicesConfigured = 64;   // device ordinals the per-device caches cover
 

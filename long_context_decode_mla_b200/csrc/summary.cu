@@ -3,7 +3,7 @@
 // group of 128 latent values and one for the 64 rope values.
 //
 //   m_d = (1/n) sum_r k_rd over the block's n rows of the request,
-//   scale_g = max_{d in g} |m_d| / 127 (1 if that is 0),
+//   scale_g = max_{d in g} |m_d| * fp32(1/127) (1 if that is 0),
 //   code_d = rint(m_d / scale_g).
 //
 // Sums are fp32 (a row's value is its code times its scale, fused into the
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(Shape<kDtype>::kStages* Shape<kDtype>::kGroupT
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float sc = amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
+        const float up = __fmul_rn(amax, kInv127), sc = up > 0.f ? up : 1.f;
         uint32_t code = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

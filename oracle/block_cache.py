@@ -43,7 +43,8 @@ def quantise_query(q):
     codes, steps = np.zeros(q.shape), np.ones((len(q), 5), np.float32)
     for g, (a, b) in enumerate(GROUPS):
         top = np.abs(q[:, a:b]).max(1)
-        steps[:, g] = np.where(top > 0, top / np.float32(127), np.float32(1))
+        up = top * (np.float32(1) / np.float32(127))
+        steps[:, g] = np.where(up > 0, up, np.float32(1))
         codes[:, a:b] = np.clip(np.rint(q[:, a:b] / steps[:, g:g + 1]), -127, 127)
     return codes, steps
 

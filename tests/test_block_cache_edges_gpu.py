@@ -107,6 +107,47 @@ def test_selection_of_many_queries(B, q_len):
     assert np.array_equal(b.cpu().numpy(), want) and np.array_equal(n.cpu().numpy(), wn)
 
 
+def _crowded_selection(B=48, H=16, stride=1024):
+    """Ranks so close together that one rounding of a step more or less changes the choice."""
+    g = torch.Generator().manual_seed(31)
+    q = torch.randn(B, 1, H, 576, generator=g).to(torch.bfloat16)
+    S = torch.zeros(stride, 608, dtype=torch.uint8)
+    S[:, :576] = torch.randint(0, 256, (stride, 576), generator=g).to(torch.uint8)
+    S[:, 576:596] = (torch.rand(stride, 5, generator=g) * 0.01 + 0.01).view(torch.uint8)
+    table = torch.arange(stride, dtype=torch.int32).repeat(B, 1)
+    lens = torch.full((B,), stride * 64, dtype=torch.int32)
+    return q, S, table, lens
+
+
+def test_selection_of_close_ranks():
+    q, S, table, lens = _crowded_selection()
+    B, stride = table.shape
+    topk = stride // 2
+    t = torch.empty(B, 1, topk, dtype=torch.int32, device="cuda")
+    b, n = torch.empty_like(t), torch.empty(B, 1, dtype=torch.int32, device="cuda")
+    ws = _u8(dcpmla.mla_block_select_workspace_size(B, q.shape[2], 1, stride))
+    dcpmla.mla_block_select(q.cuda(), S.cuda(), table.cuda(), lens.cuda(), 0, 1, topk, t, n, ws, b, 1, 1)
+    want, _ = ob.block_select(_bits(q), S.numpy(), table.numpy(), lens.numpy(), 0, 1, topk, 1, 1)
+    assert np.array_equal(b.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_summary_scale_is_one_multiplication(kv):
+    """64 equal bf16 values (fp8 rows: the rope) have an exact mean: scale = largest one * fp32(1/127), no division."""
+    n = 64
+    pool = wl.random_kv_pool(n, kv, 17)
+    pool[:] = pool[:, :1]
+    S = _u8(n * 608).view(n, 608)
+    dcpmla.mla_block_summary(pool.cuda(), kv, _i32(np.arange(n)[None]), _i32([n * 64]), 0, 1, S)
+    _, scales = ob.summary_fields(S.cpu().numpy())
+    rows = oracle.decode_rows(pool[:, 0].numpy(), kv).astype(np.float32)
+    top = np.stack([np.abs(rows[:, lo:hi]).max(1) for lo, hi in ob.GROUPS], 1)
+    if kv == "fp8":
+        top, scales = top[:, 4:], scales[:, 4:]
+    up = top * (np.float32(1) / np.float32(127))
+    assert (up != top / np.float32(127)).any() and np.array_equal(scales, up)
+
+
 def test_eviction_of_many_requests():
     B, budget = 600, 40
     g = torch.Generator().manual_seed(8)
