@@ -45,13 +45,15 @@ struct TablePieces {
 // One warp merges `count` pieces of one row into out_o (512 floats, 16-byte
 // aligned) and *out_lse (if not null): all of it, or columns [128 part, 128
 // part + 128) with kParts = 4 (part 0 writes the LSE).  The pieces are added in
-// order whatever the batch: a batch only has their loads in flight together
-// (64 pieces of one request's 64 heads, one after the other: 42 us).
+// order whatever the batch: a batch only has their loads in flight together.  The
+// quarter rows need that (64 pieces of one request's 64 heads: 42 us one after the
+// other, 18 us so); for whole rows the registers of a batch of four cost more than
+// it gives (a dense step of 32 requests and 8 shards 197 us, one by one 191 us).
 template <int kParts = 1, class Pieces>
 __device__ __forceinline__ void merge_warp(const Pieces& pc, int count, float* __restrict__ out_o,
                                            float* __restrict__ out_lse, int part = 0) {
   constexpr int kVec = 4 / kParts;               // float4 per lane
-  constexpr int kBatch = kParts == 1 ? 4 : 16;   // pieces with loads in flight
+  constexpr int kBatch = kParts == 1 ? 1 : 16;   // pieces with loads in flight
   const int lane = threadIdx.x & 31;
   const int col = part * 32 + lane;
   float M = -CUDART_INF_F;

@@ -266,7 +266,7 @@ __device__ __forceinline__ void split_hilo4(uint32_t x0, uint32_t x1, uint32_t& 
 // (flagged) loads block 0 instead and has no valid rows.  A listed tile
 // (sparse rows, p.row_ids): lanes 0..15 fetch code chunks 0 and 1 of four
 // rows each by TMA gathers; the staging warps copy the rest (listed_fetch).
-template <bool kListed>
+template <bool kListed, bool kChosen>
 __device__ __forceinline__ void producer_role(const F8Params& P, const PartialParams& p, F8Ctl& c,
                               uint8_t* base, int nseg, uint32_t& tau,
                               uint32_t (&fills)[kCodeStages]) {
@@ -274,11 +274,23 @@ __device__ __forceinline__ void producer_role(const F8Params& P, const PartialPa
   const bool lead = lane == 0;
   TileCursor cur, pf;
   if (!cur.start(p, c, nseg)) return;
-  // L2 prefetch, kPrefetchTiles ahead of the loads.  The first tile's own loads
-  // come before the first burst, which would hold them up by 2,000 cycles.
+  // L2 prefetch, kPrefetchTiles ahead of the loads.  A CTA of chosen blocks has
+  // few tiles: its first tile's own loads come before the first burst, which would
+  // hold them up by 2,000 cycles.  Long requests pay more for the loop that this
+  // takes (a 16K-token prompt's attention 39.2 ms so, 38.3 ms with the burst first).
   pf = cur;
-  bool pf_ok = !kListed && pf.next(p, c);
-  int pf_due = kPrefetchTiles;
+  bool pf_ok = !kListed;
+  int pf_due = 1;
+  if constexpr (kChosen) {
+    pf_ok = pf.next(p, c);
+    pf_due = kPrefetchTiles;
+  } else {
+    for (int i = 0; i < kPrefetchTiles && pf_ok; ++i) {
+      const int blk = tile_block(p, pf.v.b, (pf.v.row_begin >> 6) + pf.t);
+      if (lead && blk >= 0) ptx::prefetch_l2(p.kv + (size_t)blk * kTileBytes, kTileBytes);
+      pf_ok = pf.next(p, c);
+    }
+  }
   while (true) {
     const uint32_t cs = tau % kCodeStages, rs = tau % kRopeStages;
     // slot reuse: the PV of tile tau - 3 and the rope part of tile tau - 2
@@ -335,11 +347,12 @@ __device__ __forceinline__ void producer_role(const F8Params& P, const PartialPa
     }
     ++tau;
     if (!cur.next(p, c)) break;
-    for (; pf_ok && pf_due > 0; --pf_due) {
+    do {
+      if (!pf_ok) break;
       const int pb = tile_block(p, pf.v.b, (pf.v.row_begin >> 6) + pf.t);
       if (lead && pb >= 0) ptx::prefetch_l2(p.kv + (size_t)pb * kTileBytes, kTileBytes);
       pf_ok = pf.next(p, c);
-    }
+    } while (kChosen && --pf_due > 0);
     pf_due = 1;
   }
 }
@@ -652,7 +665,7 @@ __device__ __forceinline__ void staging_role(const PartialParams& p, F8Ctl& c, u
 // threads; a barrier-wide vote tells whether any thread's tile maximum
 // exceeds the max in use by more than 2^3, and only then are the maxima
 // exchanged through shared memory.
-template <bool kRound>
+template <bool kChosen>
 __device__ __forceinline__ void softmax_role(const PartialParams& p, F8Ctl& c, uint8_t* base, int nseg,
                              uint32_t& tau, uint32_t& sigma, uint32_t& pi) {
   const int T = threadIdx.x;                 // 0..255
@@ -831,7 +844,7 @@ __device__ __forceinline__ void softmax_role(const PartialParams& p, F8Ctl& c, u
       uint32_t hw[4], lw[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        split_hilo4<kRound>(hmul2_rn(pp[2 * j], swv[2 * j]), hmul2_rn(pp[2 * j + 1], swv[2 * j + 1]),
+        split_hilo4<kChosen>(hmul2_rn(pp[2 * j], swv[2 * j]), hmul2_rn(pp[2 * j + 1], swv[2 * j + 1]),
                     hw[j], lw[j]);
       *reinterpret_cast<uint4*>(pbuf + (2 * g) * kPVar + sw64(h, unit)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
       *reinterpret_cast<uint4*>(pbuf + (2 * g + 1) * kPVar + sw64(h, unit)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
@@ -908,7 +921,7 @@ __device__ __forceinline__ void block_bar() { ptx::named_bar(kBarBlock, kThreads
 // The batch loop of one side of the register split: kSoft runs the softmax
 // warps, !kSoft every other role and, at the end, the drains of the
 // asynchronous arrivals.  Both sides take the same block barriers.
-template <bool kSoft, bool kListed, bool kRound>
+template <bool kSoft, bool kListed, bool kChosen>
 __device__ __forceinline__ void run_roles(const F8Params& P, const PartialParams& p, F8Ctl& c,
                                           uint8_t* base, int lo, int hi) {
   const int warp = threadIdx.x >> 5;
@@ -921,10 +934,10 @@ __device__ __forceinline__ void run_roles(const F8Params& P, const PartialParams
     const int nseg = min(kMaxSegF8, total - first);
     if (nseg <= 0) break;
     if constexpr (kSoft) {
-      softmax_role<kRound>(p, c, base, nseg, tau, sigma, pi);
+      softmax_role<kChosen>(p, c, base, nseg, tau, sigma, pi);
     } else {
       if (warp == kProdWarp) {
-        producer_role<kListed>(P, p, c, base, nseg, tau, fills);
+        producer_role<kListed, kChosen>(P, p, c, base, nseg, tau, fills);
       } else if (warp == kQkWarp || warp == kQkWarp2) {
         if ((threadIdx.x & 31) == 0)
           qk_role<kListed>(warp == kQkWarp ? 0 : 1, p, c, base, nseg, tau, sigma);
@@ -980,7 +993,7 @@ __device__ __forceinline__ void run_roles(const F8Params& P, const PartialParams
   }
 }
 
-template <bool kListed, bool kRound>
+template <bool kListed, bool kChosen>
 __global__ void __launch_bounds__(kThreads, 1) partial_f8_kernel(const __grid_constant__ F8Params P) {
   // dense only: a known-null index list lets the compiler drop the sparse
   // branches of the shared schedule
@@ -1048,10 +1061,10 @@ __global__ void __launch_bounds__(kThreads, 1) partial_f8_kernel(const __grid_co
   // end so that each is compiled within its own budget.
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    run_roles<true, kListed, kRound>(P, p, c, base, lo, hi);
+    run_roles<true, kListed, kChosen>(P, p, c, base, lo, hi);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    run_roles<false, kListed, kRound>(P, p, c, base, lo, hi);
+    run_roles<false, kListed, kChosen>(P, p, c, base, lo, hi);
   }
   if (c.abort && threadIdx.x == 0 && p.flags) atomicOr(p.flags, kFlagTimeout);
   ptx::tc_fence_before();
