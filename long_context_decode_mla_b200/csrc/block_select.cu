@@ -190,6 +190,7 @@ struct ScoreCtl {
   int ids[2][kTile];                     // the blocks of a tile, by tile parity
   uint32_t tmem_base;
   int abort;
+  int copies_end;                        // a query image's wait gave up
   int warp_sums[16];
   int end[kRowChunk];                    // tiles up to and including each row of the chunk
   int blocks[kRowChunk];
@@ -297,7 +298,8 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
         }
       }
       if (b == 0 && tau >= (uint32_t)kScoreStages &&
-          !ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort))
+          !__all_sync(0xffffffffu,
+                      ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort)))
         return;
 #pragma unroll
       for (int i = 0; i < kCopyBatch; ++i) {
@@ -315,12 +317,15 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
     if ((t & 31) == 0) ptx::mbar_arrive(&c.full[s]);
     if (fresh) {
       if (t == 0) {
-        if (sigma > 0 && !ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort)) return;
-        ptx::wait_primary();       // the query images' kernel
-        // the scorers read the old steps through the generic proxy
-        ptx::fence_proxy_async();
-        ptx::mbar_arrive_expect_tx(&c.q_full, kQBytes);
-        ptx::bulk_g2s(ptx::smem_addr(base), p.q_codes + (size_t)r * kQBytes, kQBytes, &c.q_full);
+        if (sigma > 0 && !ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort)) {
+          c.copies_end = 1;        // the others learn of it at the barrier below
+        } else {
+          ptx::wait_primary();     // the query images' kernel
+          // the scorers read the old steps through the generic proxy
+          ptx::fence_proxy_async();
+          ptx::mbar_arrive_expect_tx(&c.q_full, kQBytes);
+          ptx::bulk_g2s(ptx::smem_addr(base), p.q_codes + (size_t)r * kQBytes, kQBytes, &c.q_full);
+        }
       }
       ++sigma;
     }
@@ -329,6 +334,7 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
     if (!more) break;
     if (t < kTile) c.ids[tau & 1][t] = next_id;
     ptx::named_bar(kBarCopy, kCopyThreads);
+    if (c.copies_end) return;
   }
 }
 
@@ -550,6 +556,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
     ptx::mbar_init(&c.q_full, 1);
     ptx::mbar_init(&c.q_empty, 1 + 8);       // the MMAs' commit, eight warps' step reads
     c.abort = 0;
+    c.copies_end = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 0) ptx::tmem_alloc(&c.tmem_base, kTmemCols);
@@ -618,7 +625,6 @@ __global__ void __launch_bounds__(topk::kThreads) choose_kernel(const SelectPara
   __shared__ topk::Ctl c;
   __shared__ float hmax[64];
   topk::cg::cluster_group cl = topk::cg::this_cluster();
-  ptx::launch_dependents();
   const int r = blockIdx.y, b = r / p.q_len;
   int nb;
   const int n = rows_of(p, r, &nb);
