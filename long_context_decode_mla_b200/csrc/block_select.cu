@@ -18,6 +18,7 @@
 #include "dcpmla.h"
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <mutex>
 
@@ -156,30 +157,37 @@ __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParam
 // summaries' codes are A (M = 128 blocks), the query's B (N = 64 heads), each
 // scale group an int32 accumulator of its own, so that a TMEM lane holds one
 // block for all heads.  Summaries are scattered over the pool: seven warps bring
-// them in 16-byte pieces into swizzled chunks (two tiles); warps 0-3
-// and 4-7 add each group's product, scaled, into the scores of 32 heads a
+// them into swizzled chunks (two tiles); warps 0-3 and 4-7 add each group's product, scaled, into the scores of 32 heads a
 // thread, which are written [head][block], and keep each head's best of a row
 // until its end.  The tiles of all rows, end to end, are dealt to the CTAs in
 // contiguous ranges, so that a CTA rarely changes query.
 //
-// What bounds it is the load/store unit's queue (copies, stores, broadcast
-// reads) and the int8 MMAs, some 3,000 cycles each for 64 blocks: M = 64 tiles
-// with a warp maximum per head and tile took 4,300 cycles for them.
+// What bounds it is the copying, some 9,000 cycles a tile of 78 KB (64 queries of
+// 1,024 blocks 24 us, of 4,096 blocks 66 us: 2.4 TB/s of summaries), then scoring
+// and the int8 MMAs, 5,000 and 4,000.
 // Sixteen warps: eight score, seven copy, one issues the MMAs; the launch gives a
 // thread 128 registers, of which the scoring warpgroups take from the others.
 constexpr int kScoreThreads = 512;
 constexpr int kCopyBase = 256, kCopyThreads = 224, kMmaWarp = 15;
 constexpr int kBarCopy = 1;
-constexpr int kLaunchRegs = 128, kScoreRegs = 168, kCopyRegs = 88;
+constexpr int kLaunchRegs = 128, kScoreRegs = 152, kCopyRegs = 104;
 static_assert(256 * (kScoreRegs + kCopyRegs) == kScoreThreads * kLaunchRegs,
               "the register split must add up to what the launch holds");
 constexpr int kUnits = kSummaryBytes / 16;         // 16-byte pieces of a summary
-constexpr int kCopyBatch = 11;                     // pieces a thread has in flight
-constexpr int kCopyBatches = (kTile * kUnits + kCopyThreads * kCopyBatch - 1) / (kCopyThreads * kCopyBatch);
+constexpr int kLoadWarps = 5;                      // of the copying threads: first these,
+constexpr int kGatherBase = 32 * kLoadWarps, kAheadBase = kGatherBase + 32;   // then a warp each
+static_assert(4 * kUnits <= kGatherBase && kAheadBase + 32 == kCopyThreads, "copy roles");
+constexpr int kCopyBatch = 8;                      // pieces of a batch, two of them in flight
+constexpr int kGatherRows = 32, kLoadRows = kTile - kGatherRows;   // of a tile's blocks
+constexpr int kLoads = kLoadRows / 4, kCopyBatches = (kLoads + kCopyBatch - 1) / kCopyBatch;
+static_assert(kGatherRows % 8 == 0 && kCopyBatch % 4 == 0 && kCopyBatches >= 2, "copy split");
 constexpr int kScoreStages = 2, kBufs = 8;
 constexpr uint32_t kSlot = 2 * kChunk;             // 128 blocks x 128 bytes
-constexpr uint32_t kScaleBytes = kTile * 32;
-constexpr uint32_t kStageBytes = kGroups * kSlot + kScaleBytes;
+// A stage: the four latent chunks, then bytes 480 to 607 of every summary: the rope's
+// codes 32 bytes into it, the scales at its end.
+constexpr int kRopeX = kSummaryBytes - 128;
+constexpr uint32_t kRopeAt = 512 - kRopeX;
+constexpr uint32_t kStageBytes = kGroups * kSlot;
 constexpr uint32_t kTmemCols = 64 * kBufs;
 constexpr int kRowChunk = kScoreThreads; // rows looked at together
 
@@ -187,10 +195,10 @@ struct ScoreCtl {
   uint64_t full[kScoreStages], empty[kScoreStages];
   uint64_t d_full[kBufs], d_empty[kBufs];
   uint64_t q_full, q_empty;
-  int ids[2][kTile];                     // the blocks of a tile, by tile parity
+  alignas(16) int ids[2][4][kTile / 4];  // the blocks of a tile, by tile parity and row % 4
   uint32_t tmem_base;
   int abort;
-  int copies_end;                        // a query image's wait gave up
+  int copies_end;                        // a copying thread's wait gave up
   int warp_sums[16];
   int end[kRowChunk];                    // tiles up to and including each row of the chunk
   int blocks[kRowChunk];
@@ -247,78 +255,127 @@ __device__ __forceinline__ float small_int(uint32_t x) {
   return __fsub_rn(__uint_as_float(0x4B400000u + x), 12582912.f);
 }
 
-// Copies of every tile (seven warps) and of each row's query image.  A tile's
-// summaries are 128 x 38 pieces, dealt to the threads in order, so that a warp
-// reads 512 bytes that mostly follow one another; a batch of them is in flight a
-// thread, the first before the stage is known to be free.  (Asynchronous 16-byte
-// copies took 40 cycles of the unit each, 8,000 a tile.)
-__device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, uint8_t* base, int r0,
-                                          int lo, int hi, uint32_t& tau, uint32_t& sigma) {
+// Copies of every tile and of each row's query image, by both ways from memory to
+// shared memory.  Five warps load the first 96 blocks through registers: thread
+// (rr, un) of 152 has piece un of the rows 4 i + rr, so that a warp reads 512 bytes
+// that mostly follow one another and a thread's addresses are sums of constants.
+// A sixth issues four-row TMA gathers of the last 32, and the seventh walks a tile
+// ahead: it looks up the blocks and sends their lines on their way to L2.  64
+// queries of 4,096 blocks: 96 us with all blocks through registers, their pieces
+// dealt to 224 threads in order, 89 as dealt here, and with 16, 24, 32, 48, 64 and 96
+// of them by gathers 82, 69, 66, 66, 81 and 98 (a gather takes some 65 cycles to
+// issue; the loads wait for one another's lines in L1, even where L2 has them all).
+__device__ __forceinline__ void copy_role(const SelectParams& p, const CUtensorMap& map, ScoreCtl& c,
+                                          uint8_t* base, int r0, int lo, int hi, uint32_t& tau,
+                                          uint32_t& sigma) {
   const int t = threadIdx.x - kCopyBase;
   TileWalk w;
   if (!w.start(c, lo, hi)) return;
   bool fresh = true;
-  // the block of row t of the walk's tile; a bad entry: a stand-in, flagged
-  auto entry = [&]() {
-    const int k = w.tile * kTile + t;
-    if (t >= kTile || k >= w.nb) return 0;
-    const int blk = __ldg(p.block_table + (size_t)((r0 + w.row) / p.q_len) * p.bt_stride + k);
-    if (blk >= 0 && (long long)blk < p.num_blocks) return blk;
-    if (p.flags) atomicOr(p.flags, kFlagBadBlock);
-    return 0;
+  // the blocks of the walk's tile; a bad entry: a stand-in, flagged
+  auto look_up = [&](uint32_t parity) {
+    const int* table = p.block_table + (size_t)((r0 + w.row) / p.q_len) * p.bt_stride;
+    int blk[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = w.tile * kTile + t - kAheadBase + 32 * e;
+      blk[e] = k < w.nb ? __ldg(table + k) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = t - kAheadBase + 32 * e;
+      const bool live = w.tile * kTile + row < w.nb;
+      if (blk[e] < 0 || (long long)blk[e] >= p.num_blocks) {
+        if (live && p.flags) atomicOr(p.flags, kFlagBadBlock);
+        blk[e] = 0;
+      }
+      c.ids[parity][row & 3][row >> 2] = blk[e];
+      if (live) {
+        const uint8_t* src = p.summaries + (size_t)blk[e] * kSummaryBytes;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) ptx::prefetch_line_l2(src + 128 * i);
+      }
+    }
   };
-  if (t < kTile) c.ids[tau & 1][t] = entry();
+  const bool ahead = t >= kAheadBase;
+  const int rr = min(t / kUnits, 3), un = t - rr * kUnits;       // un past the end: no piece
+  const uint8_t* from = p.summaries + un * 16;
+  // places of the thread's rows 0 and 4 i + rr, i = 1; two rows further: + 1024
+  const int chunk = un < 32 ? un >> 3 : 4, unit = un < 32 ? un & 7 : un - kRopeX / 16;
+  const uint32_t to0 = chunk * kSlot + qimg::sw128(rr, unit & 7);
+  const uint32_t to1 = chunk * kSlot + qimg::sw128(rr + 4, unit & 7);
+  if (ahead) look_up(tau & 1);
   ptx::named_bar(kBarCopy, kCopyThreads);
   while (true) {
     const uint32_t s = tau % kScoreStages;
-    const int* ids = c.ids[tau & 1];
     const int r = r0 + w.row;
     // rows past the tile's end are left as they are (they only reach their own lanes)
-    const int units = min(kTile, w.nb - w.tile * kTile) * kUnits;
+    const int blocks = min(kTile, w.nb - w.tile * kTile);
     const bool row_ends = w.last_of_row();
     const bool more = w.next(c);
-    const int next_id = more ? entry() : 0;
-    if (more && t < kTile && w.tile * kTile + t < w.nb) {
-      // the next tile's lines on their way to L2: a batch then waits a third as long
-      const uint8_t* src = p.summaries + (size_t)next_id * kSummaryBytes;
-#pragma unroll
-      for (int i = 0; i < 5; ++i) ptx::prefetch_line_l2(src + 128 * i);
-    }
     uint8_t* stage = base + kOffStage + s * kStageBytes;
-#pragma unroll 1
-    for (int b = 0; b < kCopyBatches; ++b) {
-      uint4 v[kCopyBatch];
-#pragma unroll
-      for (int i = 0; i < kCopyBatch; ++i) {
-        const int u = t + kCopyThreads * (b * kCopyBatch + i);
-        if (u < units) {
-          const int row = u / kUnits;
-          v[i] = __ldg(reinterpret_cast<const uint4*>(
-                           p.summaries + (size_t)ids[row] * kSummaryBytes) + (u - row * kUnits));
+    if (ahead) {
+      if (more) look_up((tau + 1) & 1);
+    } else if (t >= kGatherBase) {
+      const int lane = t - kGatherBase;
+      // groups of four blocks (past the tile's end: stand-ins, block 0)
+      const int groups = max(blocks - kLoadRows + 3, 0) / 4;
+      if (tau >= (uint32_t)kScoreStages &&
+          !__all_sync(0xffffffffu,
+                      ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort))) {
+        c.copies_end = 1;              // seen by all at the barrier below
+      } else {
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&c.full[s], groups * 4 * kGroups * 128);
+        __syncwarp();
+        for (int u = lane; u < groups * kGroups; u += 32) {
+          const int q = u / kGroups, g = u - q * kGroups, row = kLoadRows + 4 * q;
+          const int (*ids)[kTile / 4] = c.ids[tau & 1];
+          const int4 rows = make_int4(ids[0][row >> 2], ids[1][row >> 2], ids[2][row >> 2],
+                                      ids[3][row >> 2]);
+          ptx::tma_gather4(ptx::smem_addr(stage + g * kSlot + row * 128), &map,
+                           g < 4 ? g * 128 : kRopeX, rows, &c.full[s]);
         }
       }
-      if (b == 0 && tau >= (uint32_t)kScoreStages &&
+    } else {
+      const int rows = un < kUnits ? min(blocks, kLoadRows) - rr : 0;
+      const int* ids = c.ids[tau & 1][rr];
+      uint4 v[2][kCopyBatch];
+      auto load = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < kCopyBatch; i += 4) {
+          const int4 id = *reinterpret_cast<const int4*>(ids + b * kCopyBatch + i);
+          const int blk[4] = {id.x, id.y, id.z, id.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (b * kCopyBatch + i + e < kLoads && 4 * (b * kCopyBatch + i + e) < rows)
+              v[b & 1][i + e] =
+                  __ldg(reinterpret_cast<const uint4*>(from + (size_t)blk[e] * kSummaryBytes));
+        }
+      };
+      load(0);
+      load(1);
+      if (tau >= (uint32_t)kScoreStages &&
           !__all_sync(0xffffffffu,
                       ptx::mbar_wait(&c.empty[s], ((tau / kScoreStages) + 1) & 1, &c.abort)))
-        return;
+        c.copies_end = 1;              // seen by all at the barrier below
 #pragma unroll
-      for (int i = 0; i < kCopyBatch; ++i) {
-        const int u = t + kCopyThreads * (b * kCopyBatch + i);
-        if (u < units) {
-          const int row = u / kUnits, un = u - row * kUnits;
-          *reinterpret_cast<uint4*>(stage + (un < 36 ? (un >> 3) * kSlot + qimg::sw128(row, un & 7)
-                                                     : kGroups * kSlot + row * 32 + (un - 36) * 16)) =
-              v[i];
+      for (int b = 0; b < kCopyBatches; ++b) {
+        if (b > 0 && b + 1 < kCopyBatches) load(b + 1);
+#pragma unroll
+        for (int i = 0; i < kCopyBatch; ++i) {
+          const int k = b * kCopyBatch + i;
+          if (k < kLoads && 4 * k < rows)
+            *reinterpret_cast<uint4*>(stage + ((k & 1) ? to1 : to0) + (k >> 1) * 1024) = v[b & 1][i];
         }
       }
+      ptx::fence_proxy_async();          // the MMAs read through the async proxy
+      __syncwarp();
+      if ((t & 31) == 0) ptx::mbar_arrive(&c.full[s]);
     }
-    ptx::fence_proxy_async();          // the MMAs read through the async proxy
-    __syncwarp();
-    if ((t & 31) == 0) ptx::mbar_arrive(&c.full[s]);
     if (fresh) {
       if (t == 0) {
         if (sigma > 0 && !ptx::mbar_wait(&c.q_empty, (sigma - 1) & 1, &c.abort)) {
-          c.copies_end = 1;        // the others learn of it at the barrier below
+          c.copies_end = 1;
         } else {
           ptx::wait_primary();     // the query images' kernel
           // the scorers read the old steps through the generic proxy
@@ -332,7 +389,6 @@ __device__ __forceinline__ void copy_role(const SelectParams& p, ScoreCtl& c, ui
     fresh = row_ends;
     ++tau;
     if (!more) break;
-    if (t < kTile) c.ids[tau & 1][t] = next_id;
     ptx::named_bar(kBarCopy, kCopyThreads);
     if (c.copies_end) return;
   }
@@ -377,7 +433,7 @@ __device__ __forceinline__ void score_mma_role(ScoreCtl& c, uint8_t* base, int l
       for (int g = g0; g < g0 + n; ++g, ++part) {
         const uint32_t d = c.tmem_base + 64 * (part % kBufs);
         for (int ks = 0; ks < (g < 4 ? 4 : 2); ++ks)
-          ptx::mma_i8(d, dplus(dk, g * kSlot + ks * 32), dplus(dq, g * kChunk + ks * 32), kId,
+          ptx::mma_i8(d, dplus(dk, g * kSlot + (g < 4 ? 0 : kRopeAt) + ks * 32), dplus(dq, g * kChunk + ks * 32), kId,
                       ks > 0);
         ptx::mma_commit(&c.d_full[part % kBufs]);
       }
@@ -418,9 +474,10 @@ __device__ __forceinline__ void score_role(const SelectParams& p, ScoreCtl& c, u
       live = blk >= 0 && (long long)blk < p.num_blocks;
     }
     if (!ptx::mbar_wait(&c.full[s], (tau / kScoreStages) & 1, &c.abort)) return;
-    const uint8_t* sp = base + kOffStage + s * kStageBytes + kGroups * kSlot + row * 32;
-    const float4 s4 = *reinterpret_cast<const float4*>(sp);
-    const float sc[kGroups] = {s4.x, s4.y, s4.z, s4.w, *reinterpret_cast<const float*>(sp + 16)};
+    const uint8_t* sp = base + kOffStage + s * kStageBytes + (kGroups - 1) * kSlot;
+    const float4 s4 = *reinterpret_cast<const float4*>(sp + qimg::sw128(row, 6));
+    const float sc[kGroups] = {s4.x, s4.y, s4.z, s4.w,
+                               *reinterpret_cast<const float*>(sp + qimg::sw128(row, 7))};
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&c.empty[s]);
     float v[32];
@@ -480,7 +537,7 @@ __device__ __forceinline__ void block_bar() { ptx::named_bar(2, kScoreThreads); 
 // warps, else the copies and the MMAs and, at the end, the drains.  Both take the
 // same block barriers.
 template <bool kScorers>
-__device__ __forceinline__ void run_scores(const SelectParams& p, ScoreCtl& c, uint8_t* base) {
+__device__ __forceinline__ void run_scores(const SelectParams& p, const CUtensorMap& map, ScoreCtl& c, uint8_t* base) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.batch * p.q_len;
   uint32_t tau = 0, sigma = 0, part = 0;
@@ -512,7 +569,7 @@ __device__ __forceinline__ void run_scores(const SelectParams& p, ScoreCtl& c, u
       score_role(p, c, base, r0, lo, hi, tau, sigma, part);
     } else {
       if (warp < kMmaWarp)
-        copy_role(p, c, base, r0, lo, hi, tau, sigma);
+        copy_role(p, map, c, base, r0, lo, hi, tau, sigma);
       else if (lane == 0)
         score_mma_role(c, base, lo, hi, tau, sigma, part);
     }
@@ -534,10 +591,15 @@ __device__ __forceinline__ void run_scores(const SelectParams& p, ScoreCtl& c, u
     }
     if (threadIdx.x == kCopyBase && sigma > 0)
       ptx::mbar_wait(&c.q_full, (sigma - 1) & 1, &c.abort);
+    if (threadIdx.x == kCopyBase + kGatherBase)
+      for (uint32_t s = 0; s < (uint32_t)kScoreStages; ++s) {
+        const uint32_t u = tau > s ? (tau - s + kScoreStages - 1) / kScoreStages : 0;
+        if (u > 0) ptx::mbar_wait(&c.full[s], (u - 1) & 1, &c.abort);
+      }
   }
 }
 
-__global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectParams p, const __grid_constant__ CUtensorMap map) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -546,7 +608,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   ptx::launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kScoreStages; ++s) {
-      ptx::mbar_init(&c.full[s], kCopyThreads / 32);
+      ptx::mbar_init(&c.full[s], kLoadWarps + 1);
       ptx::mbar_init(&c.empty[s], 1 + 8);    // the MMAs' commit, eight warps' scale reads
     }
     for (int k = 0; k < kBufs; ++k) {
@@ -567,10 +629,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectPar
   // every warpgroup adjusts its registers here, before any role can return
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScoreRegs));
-    run_scores<true>(p, c, base);
+    run_scores<true>(p, map, c, base);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-    run_scores<false>(p, c, base);
+    run_scores<false>(p, map, c, base);
   }
   // a CTA without tiles waits too: this kernel's end implies the previous one's
   ptx::wait_primary();
@@ -767,13 +829,27 @@ int check_select(const SelectArgs& a, SelectParams* p) {
   return DCPMLA_OK;
 }
 
+// The summaries as [num_blocks][608] bytes, boxes of 128 bytes of one row (gathers).
+bool summary_map(const SelectParams& p, CUtensorMap* map) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kSummaryBytes, (cuuint64_t)std::min<long long>(p.num_blocks, INT_MAX)};
+  const cuuint64_t strides[1] = {(cuuint64_t)kSummaryBytes};
+  const cuuint32_t box[2] = {128, 1}, es[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.summaries), dims, strides,
+             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   const int rows = p.batch * p.q_len;
   q_codes_kernel<<<dim3(rows, 32), kCodeThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!summary_map(p, &map)) return cudaErrorNotSupported;
   e = launch_kernel(score_kernel, dim3((unsigned)std::min<long long>(p.num_ctas, (long long)rows * p.tiles)),
-                    kScoreThreads, kScoreSmem, st, 0, true, p);
+                    kScoreThreads, kScoreSmem, st, 0, true, p, map);
   if (e != cudaSuccess) return e;
   if (p.keys) {
     e = launch_kernel(rank_kernel, dim3((p.bt_stride + kRankThreads - 1) / kRankThreads, rows),
