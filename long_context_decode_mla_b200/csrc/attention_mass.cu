@@ -19,10 +19,11 @@
 //    decode kernel's operand image (two e4m3 terms in one power-of-two frame,
 //    q_image.cuh).  Every 128-value scale group is a part with an accumulator of
 //    its own, scaled in fp32, and the bf16 rope a fifth.
-//  * bf16 rows and queries multiply as they are (exact products), in three parts
-//    of 192 values that are added in fp32: the tensor core cuts low bits at each
-//    of its additions, and 36 in one accumulator left 2.3e-6 of the weights'
-//    error against 0.6e-6 so.
+//  * bf16 rows and queries multiply as they are (exact products), in nine parts of
+//    64 values that are added in fp32: the tensor core cuts low bits at each of its
+//    additions.  One query of 8 heads over 512 rows: 36 additions in one accumulator
+//    leave a relative error of 2.3e-6, three parts 0.63e-6, five 0.44e-6, nine
+//    0.32e-6, at the same time (58 us for 32 requests of 8,191 rows).
 //
 // A tile is two cache blocks (M = 128: a weight-stationary M = 64 MMA takes as
 // long, and 36 of them more than a block's share of HBM time).  Its rows go
@@ -67,7 +68,7 @@ struct MassParams {
 };
 
 constexpr int kThreads = 352;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;         // fp8: and warp 10
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kIssuers = 2;
 constexpr int kWeightThreads = 256;
 constexpr uint32_t kHalf = 8192;                   // 64 rows x 128 bytes
 constexpr uint32_t kSlot = 2 * kHalf;              // of a tile's two blocks
@@ -82,29 +83,28 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 template <int kDtype>
 struct Shape;
-// kMeta tiles can be between their load and their weights at once: eight slots
-// and eight accumulators hold 1.6 and 1.6 fp8 tiles, 0.9 and 2.7 bf16 tiles.
 template <>
 struct Shape<kKvFp8> {
-  static constexpr int kRowBytes = kRowBytesFp8, kChunks = 5, kParts = 5, kMeta = 4,
-                       kIssuers = 2;
+  static constexpr int kRowBytes = kRowBytesFp8, kChunks = 5;
 };
 template <>
 struct Shape<kKvBf16> {
-  static constexpr int kRowBytes = kRowBytesBf16, kChunks = 9, kParts = 3, kMeta = 10,
-                       kIssuers = 1;
+  static constexpr int kRowBytes = kRowBytesBf16, kChunks = 9;
 };
-constexpr int kMaxMeta = 10;
+// Tiles between their load and their weights: when tile t's first chunk is loaded,
+// eight slots and eight accumulators have let the weights past the rows and scales
+// of tile t - 4 (fp8: 1.6 and 1.6 tiles; bf16: 0.9 and 0.9).
+constexpr int kMeta = 4;
 constexpr uint32_t kScaleBytes = kTileMass * 16;   // fp8: four fp32 scales a row
 
 struct Ctl {
   uint64_t full[kSlots], empty[kSlots];      // a slot's bytes landed / its MMAs done
   uint64_t d_full[kBufs], d_empty[kBufs];    // an accumulator done / read
-  uint64_t meta[kMaxMeta];                   // a tile's row counts written and scales landed
+  uint64_t meta[kMeta];                      // a tile's row counts written and scales landed
   uint64_t q_full, q_empty;
   alignas(16) float2 head[64];               // 2^-a scale log2(e), lse log2(e)
   float half[2][kTileMass];                  // [tile parity]: the other half's sums
-  int nv[kMaxMeta][2];                       // rows of each block that take part
+  int nv[kMeta][2];                          // rows of each block that take part
   uint32_t tmem_base;
   int abort;
   int sel_count;
@@ -114,7 +114,7 @@ struct Ctl {
 
 template <int kDtype>
 constexpr uint32_t ctl_offset() {
-  return kQBytes + kSlots * kSlot + (kDtype == kKvFp8 ? Shape<kDtype>::kMeta * kScaleBytes : 0);
+  return kQBytes + kSlots * kSlot + (kDtype == kKvFp8 ? kMeta * kScaleBytes : 0);
 }
 template <int kDtype>
 constexpr size_t smem_bytes() {
@@ -196,7 +196,7 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
   while (true) {
     // a bad table entry: a stand-in block, no rows; a missing second block: nothing
     int blk[2], halves = 1;
-    const uint32_t meta = n.tau % S::kMeta;
+    const uint32_t meta = n.tau % kMeta;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int rows = cur.rows(i);
@@ -211,7 +211,7 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
         return;
       if (k == 0) {
         // the tile kMeta before this one has been turned into weights by now
-        // (Shape): its row counts and scales can go
+        // (kMeta): its row counts and scales can go
         c.nv[meta][0] = blk[0] >= 0 ? cur.rows(0) : 0;
         c.nv[meta][1] = blk[1] >= 0 ? cur.rows(1) : 0;
         if constexpr (kDtype == kKvFp8) {
@@ -253,9 +253,8 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
 
 // D = K Q^T (M = 128 rows, N = 64 heads, 64 TMEM columns a part).  A wait
 // costs an issuing thread some 600 cycles while the tensor core streams its
-// operands, as much as eight MMAs take: fp8 parts alternate between two issuers
-// (77 cycles an MMA, 36 a tile); one is enough for bf16 rows, whose tile has
-// twice the time, and waits for a part's three chunks at once.
+// operands, as much as eight MMAs take, so the parts alternate between two issuers
+// (77 cycles an MMA, 36 a tile; one issuer and five bf16 parts: 62 us for 58).
 template <int kDtype>
 __device__ __forceinline__ void mma_role(const MassParams& m, Ctl& c, uint8_t* base, int nseg,
                                          uint32_t side, Counts& n) {
@@ -271,63 +270,33 @@ __device__ __forceinline__ void mma_role(const MassParams& m, Ctl& c, uint8_t* b
       if (!ptx::mbar_wait(&c.q_full, n.sigma & 1, &c.abort)) return;
       ++n.sigma;
     }
-    if constexpr (kDtype == kKvFp8) {
 #pragma unroll 1
-      for (int k = 0; k < S::kChunks; ++k, ++n.chunk, ++n.part) {
-        if ((n.chunk & 1) != side) continue;
-        const uint32_t s = n.chunk % kSlots, buf = n.part % kBufs;
-        uint64_t* reuse = n.part >= (uint32_t)kBufs ? &c.d_empty[buf] : &c.full[s];
-        const uint32_t parity = (n.chunk / kSlots) & 1;
-        if (!ptx::mbar_wait3(&c.full[s], parity, reuse,
-                             n.part >= (uint32_t)kBufs ? ((n.part / kBufs) + 1) & 1 : parity,
-                             &c.full[s], parity, &c.abort))
-          return;
-        ptx::tc_fence_after();
-        const uint64_t dk = dplus(dk0, s * kSlot);
-        const uint32_t d = c.tmem_base + 64 * buf;
-        if (k < 4) {
+    for (int k = 0; k < S::kChunks; ++k, ++n.chunk, ++n.part) {
+      if ((n.chunk & 1) != side) continue;
+      const uint32_t s = n.chunk % kSlots, buf = n.part % kBufs;
+      uint64_t* reuse = n.part >= (uint32_t)kBufs ? &c.d_empty[buf] : &c.full[s];
+      const uint32_t parity = (n.chunk / kSlots) & 1;
+      if (!ptx::mbar_wait3(&c.full[s], parity, reuse,
+                           n.part >= (uint32_t)kBufs ? ((n.part / kBufs) + 1) & 1 : parity,
+                           &c.full[s], parity, &c.abort))
+        return;
+      ptx::tc_fence_after();
+      const uint64_t dk = dplus(dk0, s * kSlot);
+      const uint32_t d = c.tmem_base + 64 * buf;
+      if (kDtype == kKvFp8 && k < 4) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, k * kHalf + ks * 32), kIdF8, ks > 0);
-            ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, (4 + k) * kHalf + ks * 32), kIdF8, 1u);
-          }
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            ptx::mma_f16(d, dplus(dk, ks * 32), dplus(dq, 8 * kHalf + ks * 32), kIdBf, ks > 0);
+        for (int ks = 0; ks < 4; ++ks) {
+          ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, k * kHalf + ks * 32), kIdF8, ks > 0);
+          ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, (4 + k) * kHalf + ks * 32), kIdF8, 1u);
         }
-        ptx::mma_commit(&c.empty[s]);
-        ptx::mma_commit(&c.d_full[buf]);
+      } else {
+        const uint32_t q = (kDtype == kKvFp8 ? 8 : k) * kHalf;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          ptx::mma_f16(d, dplus(dk, ks * 32), dplus(dq, q + ks * 32), kIdBf, ks > 0);
       }
-    } else {
-#pragma unroll 1
-      for (int j = 0; j < S::kParts; ++j, ++n.part) {
-        const uint32_t buf = n.part % kBufs;
-        const bool reuse = n.part >= (uint32_t)kBufs;
-        uint64_t* bars[4];
-        uint32_t pars[4];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          bars[i] = &c.full[(n.chunk + i) % kSlots];
-          pars[i] = ((n.chunk + i) / kSlots) & 1;
-        }
-        bars[3] = reuse ? &c.d_empty[buf] : bars[0];
-        pars[3] = reuse ? ((n.part / kBufs) + 1) & 1 : pars[0];
-        if (!ptx::mbar_wait4(bars, pars, &c.abort)) return;
-        ptx::tc_fence_after();
-        const uint32_t d = c.tmem_base + 64 * buf;
-#pragma unroll 1
-        for (int i = 0; i < 3; ++i, ++n.chunk) {
-          const uint32_t s = n.chunk % kSlots;
-          const uint64_t dk = dplus(dk0, s * kSlot);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            ptx::mma_f16(d, dplus(dk, ks * 32), dplus(dq, (3 * j + i) * kHalf + ks * 32), kIdBf,
-                         (i | ks) != 0);
-          ptx::mma_commit(&c.empty[s]);
-        }
-        ptx::mma_commit(&c.d_full[buf]);
-      }
+      ptx::mma_commit(&c.empty[s]);
+      ptx::mma_commit(&c.d_full[buf]);
     }
     if (cur.last_of_segment()) ptx::mma_commit(&c.q_empty);
     ++n.tau;
@@ -371,8 +340,8 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
     }
     const long long j = (long long)(cur.v.row_begin + cur.t * kTileMass) + row;
     const int last = seq_len_of(p, b) - p.q_len;         // position of query 0
-    const uint32_t meta = n.tau % S::kMeta;
-    if (!ptx::mbar_wait(&c.meta[meta], (n.tau / S::kMeta) & 1, &c.abort)) return;
+    const uint32_t meta = n.tau % kMeta;
+    if (!ptx::mbar_wait(&c.meta[meta], (n.tau / kMeta) & 1, &c.abort)) return;
     const bool in = (row & 63) < c.nv[meta][row >> 6];
     const bool live = in && j < m.mass_stride;
     float* o = m.mass + (size_t)b * m.mass_stride + j;
@@ -393,7 +362,7 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
     const bool masked = __any_sync(0xffffffffu, from > 0);
     float v[32], sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < S::kParts; ++k) {
+    for (int k = 0; k < S::kChunks; ++k) {
       const uint32_t buf = n.part % kBufs;
       if (!ptx::mbar_wait(&c.d_full[buf], (n.part / kBufs) & 1, &c.abort)) return;
       __syncwarp();
@@ -405,7 +374,7 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&c.d_empty[buf]);
       ++n.part;
-      if (k < S::kParts - 1) {
+      if (k < S::kChunks - 1) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           if constexpr (kDtype == kKvFp8)
@@ -417,7 +386,7 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float2 f = c.head[32 * hh + e];
-          const float z = __uint_as_float(x[e]);       // the rope (fp8), the last third
+          const float z = __uint_as_float(x[e]);       // the rope
           const float y = kDtype == kKvFp8 ? fmaf(f.x, v[e], fmaf(sl2, z, -f.y))
                                            : fmaf(f.x, v[e] + z, -f.y);
           float w = ex2(y);
@@ -466,9 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       ptx::mbar_init(&c.d_full[k], 1);
       ptx::mbar_init(&c.d_empty[k], kWeightThreads / 32);
     }
-    for (int k = 0; k < S::kMeta; ++k) ptx::mbar_init(&c.meta[k], 1);
+    for (int k = 0; k < kMeta; ++k) ptx::mbar_init(&c.meta[k], 1);
     ptx::mbar_init(&c.q_full, 1);
-    ptx::mbar_init(&c.q_empty, S::kIssuers);
+    ptx::mbar_init(&c.q_empty, kIssuers);
     c.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -493,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     } else if (warp == kLoadWarp) {
       if ((threadIdx.x & 31) == 0) load_role<kDtype>(m, c, base, nseg, n);
     } else {
-      if ((threadIdx.x & 31) == 0 && warp < kMmaWarp + S::kIssuers)
+      if ((threadIdx.x & 31) == 0 && warp < kMmaWarp + kIssuers)
         mma_role<kDtype>(m, c, base, nseg, warp - kMmaWarp, n);
     }
     __syncthreads();
@@ -505,14 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   ptx::wait_primary();
   // Drain: every asynchronous arrival lands before the CTA exits (after a
   // timeout these waits are bounded too).
-  if ((threadIdx.x & 31) == 0 && warp >= kMmaWarp && warp < kMmaWarp + S::kIssuers) {
+  if ((threadIdx.x & 31) == 0 && warp >= kMmaWarp && warp < kMmaWarp + kIssuers) {
     drain(c.empty, kSlots, n.chunk, c);
     drain(c.d_full, kBufs, n.part, c);
     if (n.sigma > 0) ptx::mbar_wait(&c.q_empty, (n.sigma - 1) & 1, &c.abort);
   }
   if (threadIdx.x == kLoadWarp * 32) {
     drain(c.full, kSlots, n.chunk, c);
-    drain(c.meta, S::kMeta, n.tau, c);
+    drain(c.meta, kMeta, n.tau, c);
     if (n.sigma > 0) ptx::mbar_wait(&c.q_full, (n.sigma - 1) & 1, &c.abort);
   }
   ptx::tc_fence_before();
