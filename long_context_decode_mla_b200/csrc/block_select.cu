@@ -80,74 +80,86 @@ __device__ __forceinline__ int rows_of(const SelectParams& p, int r, int* blocks
   return n;
 }
 
-// Query images of two heads of one row: a warp per head and scale group, four
-// values a lane (the IEEE divisions are what it spends its time on: 72 of them a
-// thread took 9 us).  With an e4m3 cache the decode kernel's Q image (its layout
-// and rules: q_image.cuh) is built from the same loads.
-constexpr int kCodeThreads = 2 * kGroups * 32;
+// Query images of four heads of one row: half a warp per head and scale group, eight
+// values a lane (its issue slots are what bounds it: 64 queries of 64 heads 7.2 us,
+// with four values a lane 7.9, with 72 9; 48 of 16 heads 4.7 and 6.3).  With an e4m3 cache the decode kernel's Q
+// image (its layout and rules: q_image.cuh) is built from the same loads.
+constexpr int kCodeHeads = 4, kCodeThreads = kCodeHeads / 2 * kGroups * 32;
 __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParams p) {
   ptx::launch_dependents();
-  __shared__ uint32_t top[2][4];        // latent: largest |q| bits of each group
-  const int r = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int half = warp / kGroups, g = warp % kGroups, h = blockIdx.y * 2 + half;
+  __shared__ uint32_t top[kCodeHeads][4];        // latent: largest |q| bits of each group
+  const int r = blockIdx.x, warp = threadIdx.x >> 5, l = threadIdx.x & 15;
+  const uint32_t lanes = (threadIdx.x & 16) ? 0xFFFF0000u : 0xFFFFu;     // of this head
+  const int hh = warp / kGroups * 2 + ((threadIdx.x >> 4) & 1), g = warp % kGroups;
+  const int h = blockIdx.y * kCodeHeads + hh;
   const bool live = h < p.heads;
   const __nv_bfloat16* q =
       p.q + ((size_t)r * p.heads + (live ? h : 0)) * kHeadDim + 128 * g;
-  const int d = (g < 4 ? 4 : 2) * lane;
-  uint2 w = make_uint2(0, 0);
+  const int d = (g < 4 ? 8 : 4) * l;             // first of the lane's values
+  uint4 w = make_uint4(0, 0, 0, 0);
   if (live) {
-    if (g < 4)
-      w = __ldg(reinterpret_cast<const uint2*>(q + d));
-    else
-      w.x = __ldg(reinterpret_cast<const uint32_t*>(q + d));
+    if (g < 4) {
+      w = __ldg(reinterpret_cast<const uint4*>(q + d));
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(q + d));
+      w.x = v.x;
+      w.y = v.y;
+    }
   }
-  float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+  float x[8];
   uint32_t finite = 0, any = 0;         // largest magnitudes, as bits: finite ones, all but NaN
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t m = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t u = e & 1 ? words[e >> 1] & 0xFFFF0000u : words[e >> 1] << 16;
+    const uint32_t m = u & 0x7FFFFFFFu;
     if (m <= 0x7F800000u) any = max(any, m);
-    if (m < 0x7F800000u)
-      finite = max(finite, m);
-    else
-      x[e] = 0.f;
+    if (m < 0x7F800000u) finite = max(finite, m);
+    x[e] = m < 0x7F800000u ? __uint_as_float(u) : 0.f;
   }
-  finite = __reduce_max_sync(0xffffffffu, finite);
+  finite = __reduce_max_sync(lanes, finite);
   const float amax = __uint_as_float(finite);
   const float up = __fmul_rn(amax, kInv127), step = up > 0.f ? up : 1.f;
-  uint32_t code = 0;
+  const float inv = __frcp_rn(step);
+  uint32_t code[2] = {0, 0};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int c = min(127, max(-127, __float2int_rn(__fdiv_rn(x[e], step))));
-    code |= ((uint32_t)c & 0xFFu) << (8 * e);
+  for (int e = 0; e < 8; ++e) {
+    // x / step, to the nearest: the product with the reciprocal is within 2^-16 of the
+    // quotient (magnitudes up to 127); near a half, or where the reciprocal overflowed,
+    // the division decides
+    float c = rintf(__fmul_rn(x[e], inv));
+    if (!(fabsf(__fsub_rn(__fmul_rn(x[e], inv), c)) < 0.4999f)) c = rintf(__fdiv_rn(x[e], step));
+    code[e >> 2] |= ((uint32_t)min(127, max(-127, (int)c)) & 0xFFu) << (8 * (e & 3));
   }
   uint8_t* out = p.q_codes + (size_t)r * kQBytes;
   const uint32_t at = g * kChunk + qimg::sw128(h, d >> 4) + (d & 15);
   if (g < 4)
-    *reinterpret_cast<uint32_t*>(out + at) = code;
+    *reinterpret_cast<uint2*>(out + at) = make_uint2(code[0], code[1]);
   else
-    *reinterpret_cast<uint16_t*>(out + at) = (uint16_t)code;
-  if (lane == 0) {
+    *reinterpret_cast<uint32_t*>(out + at) = code[0];
+  if (l == 0) {
     reinterpret_cast<float*>(out + kQCodes)[g * 64 + h] = step;
     if (g == 0) p.row_max[(size_t)r * 64 + h] = 0u;      // below every score's key
   }
   if (!p.q_image) return;
-  any = __reduce_max_sync(0xffffffffu, any);
-  if (lane == 0 && g < 4) top[half][g] = any;
+  any = __reduce_max_sync(lanes, any);
+  if (l == 0 && g < 4) top[hh][g] = any;
   __syncthreads();
   uint8_t* img = p.q_image + (size_t)r * kQImageBytes;
   if (g == 4) {
-    *reinterpret_cast<uint32_t*>(img + qimg::kRope + qimg::sw128(h, d >> 3) + 2 * (d & 7)) = w.x;
+    *reinterpret_cast<uint2*>(img + qimg::kRope + qimg::sw128(h, d >> 3) + 2 * (d & 7)) =
+        make_uint2(w.x, w.y);
     return;
   }
-  const uint32_t m = max(max(top[half][0], top[half][1]), max(top[half][2], top[half][3]));
+  const uint32_t m = max(max(top[hh][0], top[hh][1]), max(top[hh][2], top[hh][3]));
   const int a = m > 0 ? min(120, max(-120, 7 - ((int)(m >> 23) - 127))) : 0;
-  uint32_t hi, lo;
-  qimg::split_q4(w.x, w.y, __uint_as_float((uint32_t)(127 + a) << 23), hi, lo);
-  *reinterpret_cast<uint32_t*>(img + qimg::kHi + at) = hi;
-  *reinterpret_cast<uint32_t*>(img + qimg::kLo + at) = lo;
-  if (lane == 0 && g == 0)
+  const float fa = __uint_as_float((uint32_t)(127 + a) << 23);
+  uint2 hi, lo;
+  qimg::split_q4(w.x, w.y, fa, hi.x, lo.x);
+  qimg::split_q4(w.z, w.w, fa, hi.y, lo.y);
+  *reinterpret_cast<uint2*>(img + qimg::kHi + at) = hi;
+  *reinterpret_cast<uint2*>(img + qimg::kLo + at) = lo;
+  if (l == 0 && g == 0)
     reinterpret_cast<float*>(img + qimg::kFrame)[h] = __uint_as_float((uint32_t)(127 - a) << 23);
 }
 
@@ -843,7 +855,7 @@ bool summary_map(const SelectParams& p, CUtensorMap* map) {
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   const int rows = p.batch * p.q_len;
-  q_codes_kernel<<<dim3(rows, 32), kCodeThreads, 0, st>>>(p);
+  q_codes_kernel<<<dim3(rows, kMaxHeads / kCodeHeads), kCodeThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   CUtensorMap map;
