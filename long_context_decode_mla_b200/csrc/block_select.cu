@@ -82,8 +82,9 @@ __device__ __forceinline__ int rows_of(const SelectParams& p, int r, int* blocks
 
 // Query images of four heads of one row: half a warp per head and scale group, eight
 // values a lane (its issue slots are what bounds it: 64 queries of 64 heads 7.2 us,
-// with four values a lane 7.9, with 72 9; 48 of 16 heads 4.7 and 6.3).  With an e4m3 cache the decode kernel's Q
-// image (its layout and rules: q_image.cuh) is built from the same loads.
+// with four values a lane 7.9, with 72 9; 48 of 16 heads 4.7 and 6.3).  With an
+// e4m3 cache the decode kernel's Q image (its layout and rules: q_image.cuh) is built
+// from the same loads.
 constexpr int kCodeHeads = 4, kCodeThreads = kCodeHeads / 2 * kGroups * 32;
 __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParams p) {
   ptx::launch_dependents();

@@ -88,9 +88,10 @@ cudaError_t launch_dcp_merge(const float* partials, const float* lses, int num_s
 cudaError_t launch_split_combine(const PartialParams& p, cudaStream_t st) {
   if ((p.sparse_idx && p.sparse_parts == 1) || p.request_aligned) return cudaSuccess;
   // one or two requests have many pieces each and few heads to spread them over:
-  // four warps a head then (one request of 64 heads and 64 pieces: 42 us one piece
-  // after the other, 18 us so); with 48 requests of 16 heads the look at the
-  // lengths by four times the CTAs costs more than it gains (5 against 12 us)
+  // four warps a head then (one request of 64 heads and 64 pieces: 42 us by one warp a
+  // head, 18 us so, before the weights were a lane's each); with 48 requests of 16
+  // heads the look at the lengths by four times the CTAs costs more than it gains (5
+  // against 12 us)
   if ((long long)p.batch * p.heads <= 128)
     split_combine_kernel<4><<<p.batch * ((p.heads + 1) / 2), 256, 0, st>>>(p);
   else

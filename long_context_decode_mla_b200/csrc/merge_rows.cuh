@@ -45,15 +45,17 @@ struct TablePieces {
 // One warp merges `count` pieces of one row into out_o (512 floats, 16-byte
 // aligned) and *out_lse (if not null): all of it, or columns [128 part, 128
 // part + 128) with kParts = 4 (part 0 writes the LSE).  The pieces are added in
-// order whatever the batch: a batch only has their loads in flight together.  The
-// quarter rows need that (64 pieces of one request's 64 heads: 42 us one after the
-// other, 18 us so); for whole rows the registers of a batch of four cost more than
-// it gives (a dense step of 32 requests and 8 shards 197 us, one by one 191 us).
+// order whatever the batch, each lane working out the weights of its own pieces:
+// this runs once from cold instruction caches, and its length is what it costs (one
+// request's 64 heads and 32 pieces: 10.5 us with an expf per piece and lane, 6.6 so,
+// by 8, 16 or 32 loads in flight; 42 us one piece after the other).  For whole rows
+// the registers of four pieces cost more than they give (a dense step of 32 requests
+// and 8 shards 195 us, one by one 191 us).
 template <int kParts = 1, class Pieces>
 __device__ __forceinline__ void merge_warp(const Pieces& pc, int count, float* __restrict__ out_o,
                                            float* __restrict__ out_lse, int part = 0) {
   constexpr int kVec = 4 / kParts;               // float4 per lane
-  constexpr int kBatch = kParts == 1 ? 1 : 16;   // pieces with loads in flight
+  constexpr int kBatch = kParts == 1 ? 1 : 8;    // pieces with loads in flight
   const int lane = threadIdx.x & 31;
   const int col = part * 32 + lane;
   float M = -CUDART_INF_F;
@@ -73,24 +75,22 @@ __device__ __forceinline__ void merge_warp(const Pieces& pc, int count, float* _
   for (int k0 = 0; k0 < count; k0 += 32) {
     const float mine = k0 + lane < count ? pc.lse_of(k0 + lane) : -CUDART_INF_F;
     const int n = min(32, count - k0);
+    // a lane each: the piece's weight (0 past the end), and whether it has one
+    const float weight = expf(mine - M);
+    const unsigned live = __ballot_sync(0xffffffffu, mine != -CUDART_INF_F);
     for (int j0 = 0; j0 < n; j0 += kBatch) {
-      float lk[kBatch];
       float4 v[kBatch][kVec];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        // past the end: the lane holds -inf
-        lk[j] = __shfl_sync(0xffffffffu, mine, (j0 + j) & 31);
-        if (j0 + j >= n) lk[j] = -CUDART_INF_F;
-        if (lk[j] != -CUDART_INF_F) {
-          const float4* src = pc.row(k0 + j0 + j);
+        if (!(live >> (j0 + j) & 1u)) continue;
+        const float4* src = pc.row(k0 + j0 + j);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] = __ldg(src + i * 32 + col);
-        }
+        for (int i = 0; i < kVec; ++i) v[j][i] = __ldg(src + i * 32 + col);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        if (lk[j] == -CUDART_INF_F) continue;
-        const float w = expf(lk[j] - M);
+        if (!(live >> (j0 + j) & 1u)) continue;
+        const float w = __shfl_sync(0xffffffffu, weight, j0 + j);
         wsum += w;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
