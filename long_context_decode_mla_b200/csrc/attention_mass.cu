@@ -15,10 +15,12 @@
 // but for one exchange between two.  Rows past a
 // request's end only ever reach their own lanes, so nothing is cleared.
 //
-//  * fp8 rows: the e4m3 codes are the A operand as they are; Q comes as the
-//    decode kernel's operand image (two e4m3 terms in one power-of-two frame,
-//    q_image.cuh).  Every 128-value scale group is a part with an accumulator of
-//    its own, scaled in fp32, and the bf16 rope a fifth.
+//  * fp8 rows: the e4m3 codes are the A operand as they are; Q comes as two e4m3
+//    terms in one power-of-two frame (q_image.cuh), 128 rows of one operand with an
+//    accumulator each, the second times 2^4: in one accumulator, and so in one
+//    frame, the format's smallest step left 1e-6 to 6e-6 of a query's weights as
+//    error, a head's own, which no sum over rows averages away.  Every 128-value
+//    scale group is a part, scaled in fp32, and the bf16 rope a fifth.
 //  * bf16 rows and queries multiply as they are (exact products), in nine parts of
 //    64 values that are added in fp32: the tensor core cuts low bits at each of its
 //    additions.  One query of 8 heads over 512 rows: 36 additions in one accumulator
@@ -73,8 +75,9 @@ constexpr int kWeightThreads = 256;
 constexpr uint32_t kHalf = 8192;                   // 64 rows x 128 bytes
 constexpr uint32_t kSlot = 2 * kHalf;              // of a tile's two blocks
 constexpr int kSlots = 8;
-constexpr int kBufs = 8;                           // TMEM accumulators of 64 columns
-constexpr uint32_t kTmemCols = 64 * kBufs;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxBufs = 8;
+constexpr int kLoBits = 4;                         // Q's second e4m3 term is times 2^4
 constexpr uint32_t kQBytes = 9 * kHalf;            // fp8: hi, lo, rope; bf16: nine chunks
 constexpr int kPrefetchTiles = 1;                  // more crowd the L2: 61 us at 1, 86 at 4
 constexpr int kMaxSeg = 64;
@@ -85,21 +88,21 @@ template <int kDtype>
 struct Shape;
 template <>
 struct Shape<kKvFp8> {
-  static constexpr int kRowBytes = kRowBytesFp8, kChunks = 5;
+  static constexpr int kRowBytes = kRowBytesFp8, kChunks = 5, kBufs = 4;    // 128 columns
 };
 template <>
 struct Shape<kKvBf16> {
-  static constexpr int kRowBytes = kRowBytesBf16, kChunks = 9;
+  static constexpr int kRowBytes = kRowBytesBf16, kChunks = 9, kBufs = 8;   // 64 columns
 };
 // Tiles between their load and their weights: when tile t's first chunk is loaded,
-// eight slots and eight accumulators have let the weights past the rows and scales
-// of tile t - 4 (fp8: 1.6 and 1.6 tiles; bf16: 0.9 and 0.9).
+// the slots and accumulators have let the weights past the rows and scales of tile
+// t - 4 (fp8: 1.6 and 0.8 tiles; bf16: 0.9 and 0.9).
 constexpr int kMeta = 4;
 constexpr uint32_t kScaleBytes = kTileMass * 16;   // fp8: four fp32 scales a row
 
 struct Ctl {
   uint64_t full[kSlots], empty[kSlots];      // a slot's bytes landed / its MMAs done
-  uint64_t d_full[kBufs], d_empty[kBufs];    // an accumulator done / read
+  uint64_t d_full[kMaxBufs], d_empty[kMaxBufs];    // an accumulator done / read
   uint64_t meta[kMeta];                      // a tile's row counts written and scales landed
   uint64_t q_full, q_empty;
   alignas(16) float2 head[64];               // 2^-a scale log2(e), lse log2(e)
@@ -235,7 +238,12 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
         ptx::mbar_arrive_expect_tx(&c.q_full, kQBytes);
         if constexpr (kDtype == kKvFp8) {
           ptx::wait_primary();       // the images' kernel
-          ptx::bulk_g2s(dq, p.q_image + (size_t)cur.v.b * kQImageBytes, kQBytes, &c.q_full);
+          // the two terms of a group one after the other: 128 rows of one operand
+          const uint8_t* image = p.q_image + (size_t)cur.v.b * kQImageBytes;
+#pragma unroll 1
+          for (int j = 0; j < 9; ++j)
+            ptx::bulk_g2s(dq + (j < 4 ? 2 * j : j < 8 ? 2 * j - 7 : 8) * kHalf, image + j * kHalf,
+                          kHalf, &c.q_full);
         } else {
 #pragma unroll 1
           for (int j = 0; j < 9; ++j)
@@ -251,15 +259,15 @@ __device__ __forceinline__ void load_role(const MassParams& m, Ctl& c, uint8_t* 
   }
 }
 
-// D = K Q^T (M = 128 rows, N = 64 heads, 64 TMEM columns a part).  A wait
-// costs an issuing thread some 600 cycles while the tensor core streams its
-// operands, as much as eight MMAs take, so the parts alternate between two issuers
-// (77 cycles an MMA, 36 a tile; one issuer and five bf16 parts: 62 us for 58).
+// D = K Q^T (M = 128 rows, N = 64 heads, or 128: both terms of 64).  A wait costs an
+// issuing thread some 600 cycles while the tensor core streams its operands, as much
+// as eight MMAs take, so the parts alternate between two issuers (bf16 rows with one
+// issuer and five parts: 62 us for 58).
 template <int kDtype>
 __device__ __forceinline__ void mma_role(const MassParams& m, Ctl& c, uint8_t* base, int nseg,
                                          uint32_t side, Counts& n) {
   using S = Shape<kDtype>;
-  constexpr uint32_t kIdF8 = ptx::idesc_make(128, 64, 0, false, false);
+  constexpr uint32_t kIdF8 = ptx::idesc_make(128, 128, 0, false, false);    // both terms of Q
   constexpr uint32_t kIdBf = ptx::idesc_make(128, 64, 1, false, false);
   const uint64_t dq = ptx::sdesc(ptx::smem_addr(base), 16, 1024, ptx::kSwizzle128B);
   const uint64_t dk0 = ptx::sdesc(ptx::smem_addr(base + kOffSlot), 16, 1024, ptx::kSwizzle128B);
@@ -273,22 +281,20 @@ __device__ __forceinline__ void mma_role(const MassParams& m, Ctl& c, uint8_t* b
 #pragma unroll 1
     for (int k = 0; k < S::kChunks; ++k, ++n.chunk, ++n.part) {
       if ((n.chunk & 1) != side) continue;
-      const uint32_t s = n.chunk % kSlots, buf = n.part % kBufs;
-      uint64_t* reuse = n.part >= (uint32_t)kBufs ? &c.d_empty[buf] : &c.full[s];
+      const uint32_t s = n.chunk % kSlots, buf = n.part % S::kBufs;
+      uint64_t* reuse = n.part >= (uint32_t)S::kBufs ? &c.d_empty[buf] : &c.full[s];
       const uint32_t parity = (n.chunk / kSlots) & 1;
       if (!ptx::mbar_wait3(&c.full[s], parity, reuse,
-                           n.part >= (uint32_t)kBufs ? ((n.part / kBufs) + 1) & 1 : parity,
+                           n.part >= (uint32_t)S::kBufs ? ((n.part / S::kBufs) + 1) & 1 : parity,
                            &c.full[s], parity, &c.abort))
         return;
       ptx::tc_fence_after();
       const uint64_t dk = dplus(dk0, s * kSlot);
-      const uint32_t d = c.tmem_base + 64 * buf;
+      const uint32_t d = c.tmem_base + kTmemCols / S::kBufs * buf;
       if (kDtype == kKvFp8 && k < 4) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, k * kHalf + ks * 32), kIdF8, ks > 0);
-          ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, (4 + k) * kHalf + ks * 32), kIdF8, 1u);
-        }
+        for (int ks = 0; ks < 4; ++ks)
+          ptx::mma_f8(d, dplus(dk, ks * 32), dplus(dq, 2 * k * kHalf + ks * 32), kIdF8, ks > 0);
       } else {
         const uint32_t q = (kDtype == kKvFp8 ? 8 : k) * kHalf;
 #pragma unroll
@@ -363,12 +369,14 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
     float v[32], sum = 0.f;
 #pragma unroll
     for (int k = 0; k < S::kChunks; ++k) {
-      const uint32_t buf = n.part % kBufs;
-      if (!ptx::mbar_wait(&c.d_full[buf], (n.part / kBufs) & 1, &c.abort)) return;
+      const uint32_t buf = n.part % S::kBufs, at = lane_base + kTmemCols / S::kBufs * buf;
+      const bool two = kDtype == kKvFp8 && k < S::kChunks - 1;     // accumulators
+      if (!ptx::mbar_wait(&c.d_full[buf], (n.part / S::kBufs) & 1, &c.abort)) return;
       __syncwarp();
       ptx::tc_fence_after();
-      uint32_t x[32];
-      ptx::tmem_ld32(lane_base + 64 * buf, x);
+      uint32_t x[32], lo[32];
+      ptx::tmem_ld32(at, x);
+      if (two) ptx::tmem_ld32(at + 64, lo);
       ptx::tmem_wait_ld();
       ptx::tc_fence_before();
       __syncwarp();
@@ -377,11 +385,12 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
       if (k < S::kChunks - 1) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          if constexpr (kDtype == kKvFp8)
-            v[e] = k == 0 ? sc[0] * __uint_as_float(x[e])
-                          : fmaf(sc[k & 3], __uint_as_float(x[e]), v[e]);
-          else
+          if constexpr (kDtype == kKvFp8) {
+            const float s = fmaf(__uint_as_float(lo[e]), 1.f / (1 << kLoBits), __uint_as_float(x[e]));
+            v[e] = k == 0 ? sc[0] * s : fmaf(sc[k & 3], s, v[e]);
+          } else {
             v[e] = k == 0 ? __uint_as_float(x[e]) : v[e] + __uint_as_float(x[e]);
+          }
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       ptx::mbar_init(&c.full[s], 1);
       ptx::mbar_init(&c.empty[s], 1);
     }
-    for (int k = 0; k < kBufs; ++k) {
+    for (int k = 0; k < S::kBufs; ++k) {
       ptx::mbar_init(&c.d_full[k], 1);
       ptx::mbar_init(&c.d_empty[k], kWeightThreads / 32);
     }
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   // timeout these waits are bounded too).
   if ((threadIdx.x & 31) == 0 && warp >= kMmaWarp && warp < kMmaWarp + kIssuers) {
     drain(c.empty, kSlots, n.chunk, c);
-    drain(c.d_full, kBufs, n.part, c);
+    drain(c.d_full, S::kBufs, n.part, c);
     if (n.sigma > 0) ptx::mbar_wait(&c.q_empty, (n.sigma - 1) & 1, &c.abort);
   }
   if (threadIdx.x == kLoadWarp * 32) {
@@ -489,6 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   ptx::tc_fence_after();
   if (c.abort && threadIdx.x == 0 && p.flags) atomicOr(p.flags, DCPMLA_FLAG_TIMEOUT);
   if (warp == 0) ptx::tmem_dealloc(c.tmem_base, kTmemCols);
+}
+
+// Q operand images of every request (q_image.cuh), the second term times 2^kLoBits.
+// Grid (batch, 2): each CTA covers 32 head rows with 8 threads per head.
+__global__ void __launch_bounds__(256) mass_q_image_kernel(const PartialParams p, uint8_t* image) {
+  ptx::launch_dependents();
+  qimg::build_q_image_row<kLoBits>(p.q, p.rows_q, p.heads, blockIdx.x,
+                                   blockIdx.y * 32 + (threadIdx.x >> 3), threadIdx.x & 7, image);
 }
 
 // ---------------------------------------------------------------- host -----
@@ -532,7 +549,8 @@ cudaError_t launch_mass(MassParams& m, int dev, cudaStream_t st) {
     }
   }
   if (kDtype == kKvFp8) {
-    const cudaError_t e = launch_q_image(p, st);
+    mass_q_image_kernel<<<dim3(p.batch, 2), 256, 0, st>>>(p, p.q_image);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return launch_kernel(mass_kernel<kDtype>, dim3(p.num_ctas), kThreads, smem, st, 0,

@@ -45,9 +45,6 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn tensor_map_encoder();
 
-// Q operand images of every request into p.q_image (q_image.cuh).
-cudaError_t launch_q_image(const PartialParams& p, cudaStream_t st);
-
 cudaError_t launch_partial_simt(const PartialParams& p, int kv_dtype, cudaStream_t st);
 cudaError_t launch_partial_tc(const PartialParams& p, int kv_dtype, cudaStream_t st);
 bool tc_supports(const PartialParams& p, int kv_dtype);

@@ -1078,7 +1078,6 @@ __global__ void __launch_bounds__(kThreads, 1) partial_f8_kernel(const __grid_co
 // Q operand images of every request (q_image.cuh).  Grid (batch, 2): each CTA
 // covers 32 head rows with 8 threads per head.
 __global__ void __launch_bounds__(256) f8_q_image_kernel(const PartialParams p, uint8_t* image) {
-  ptx::launch_dependents();
   qimg::build_q_image_row(p.q, p.rows_q, p.heads, blockIdx.x,
                           blockIdx.y * 32 + (threadIdx.x >> 3), threadIdx.x & 7, image);
 }
@@ -1137,11 +1136,6 @@ EncodeTiledFn tensor_map_encoder() {
   return fn;
 }
 
-cudaError_t launch_q_image(const PartialParams& p, cudaStream_t st) {
-  f8_q_image_kernel<<<dim3(p.batch, 2), 256, 0, st>>>(p, p.q_image);
-  return cudaGetLastError();
-}
-
 bool f8_supports(const PartialParams& p, int kv_dtype) {
   return kv_dtype == kKvFp8 && p.q_len == 1 && p.heads >= 1 && p.heads <= kMaxHeads &&
          p.sparse_idx == nullptr && tensor_map_encoder() != nullptr;
@@ -1181,10 +1175,7 @@ cudaError_t launch_partial_f8(const PartialParams& p, cudaStream_t st) {
       g_attr_done[form][dev] = true;
     }
   }
-  if (!p.q_image_ready) {
-    e = launch_q_image(p, st);
-    if (e != cudaSuccess) return e;
-  }
+  if (!p.q_image_ready) f8_q_image_kernel<<<dim3(p.batch, 2), 256, 0, st>>>(p, p.q_image);
   kernel<<<p.num_ctas, kThreads, smem, st>>>(fp);
   return cudaGetLastError();
 }

@@ -49,9 +49,13 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t pair) {
 // Two words of bf16 pairs (four values) times the frame 2^a -> the e4m3 codes
 // of the four values (hi) and the e4m3 codes of what hi leaves of them (lo),
 // first value in the low byte.  The product is exact (a power of two within
-// range) and so is the remainder.
+// range) and so is the remainder.  With kLoBits the remainder is encoded times
+// 2^kLoBits: at most 2^-4 of the value, it stays in range with 4, and values far
+// below the largest keep 4 more of the bits that end at the format's 2^-9.
+template <int kLoBits = 0>
 __device__ __forceinline__ void split_q4(uint32_t w0, uint32_t w1, float fa, uint32_t& hi,
                                          uint32_t& lo) {
+  constexpr float kUp = 1 << kLoBits;
   const float f0 = __uint_as_float(w0 << 16) * fa;
   const float f1 = __uint_as_float(w0 & 0xFFFF0000u) * fa;
   const float f2 = __uint_as_float(w1 << 16) * fa;
@@ -59,7 +63,8 @@ __device__ __forceinline__ void split_q4(uint32_t w0, uint32_t w1, float fa, uin
   const uint32_t h01 = e4m3x2_f32(f0, f1), h23 = e4m3x2_f32(f2, f3);
   const float2 b01 = e4m3x2_to_f32(h01), b23 = e4m3x2_to_f32(h23);
   hi = h01 | (h23 << 16);
-  lo = e4m3x2_f32(f0 - b01.x, f1 - b01.y) | (e4m3x2_f32(f2 - b23.x, f3 - b23.y) << 16);
+  lo = e4m3x2_f32((f0 - b01.x) * kUp, (f1 - b01.y) * kUp) |
+       (e4m3x2_f32((f2 - b23.x) * kUp, (f3 - b23.y) * kUp) << 16);
 }
 
 // One thread's share of request b's image: head row h (< 64), part t (0..7,
@@ -67,6 +72,7 @@ __device__ __forceinline__ void split_q4(uint32_t w0, uint32_t w1, float fa, uin
 // calling together): latent values [64 t, 64 t + 64) (four 16-value units of
 // group t / 2) and rope unit t.  All of the thread's loads are issued before
 // any use.
+template <int kLoBits = 0>
 __device__ __forceinline__ void build_q_image_row(const __nv_bfloat16* q, int rows_q, int heads,
                                                   int b, int h, int t, uint8_t* image) {
   const bool live = h < heads;
@@ -102,10 +108,10 @@ __device__ __forceinline__ void build_q_image_row(const __nv_bfloat16* q, int ro
     const int un = (t & 1) * 4 + j;
     const uint4 x0 = v[2 * j], x1 = v[2 * j + 1];
     uint4 hi, lo;
-    split_q4(x0.x, x0.y, fa, hi.x, lo.x);
-    split_q4(x0.z, x0.w, fa, hi.y, lo.y);
-    split_q4(x1.x, x1.y, fa, hi.z, lo.z);
-    split_q4(x1.z, x1.w, fa, hi.w, lo.w);
+    split_q4<kLoBits>(x0.x, x0.y, fa, hi.x, lo.x);
+    split_q4<kLoBits>(x0.z, x0.w, fa, hi.y, lo.y);
+    split_q4<kLoBits>(x1.x, x1.y, fa, hi.z, lo.z);
+    split_q4<kLoBits>(x1.z, x1.w, fa, hi.w, lo.w);
     *reinterpret_cast<uint4*>(img + kHi + g * kChunk + sw128(h, un)) = hi;
     *reinterpret_cast<uint4*>(img + kLo + g * kChunk + sw128(h, un)) = lo;
   }

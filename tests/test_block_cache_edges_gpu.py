@@ -67,6 +67,26 @@ def test_mass_of_many_small_requests(kv, B, splits):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_mass_of_one_head(kv):
+    """One head's weights keep their relative error: no other head's, and no sum over rows, averages it away."""
+    B, n = 64, 64
+    pool = wl.random_kv_pool(B, kv, 71)
+    q = torch.randn(B, 1, 576, generator=torch.Generator().manual_seed(72)).to(torch.bfloat16)
+    table = torch.arange(B, dtype=torch.int32)[:, None].contiguous()
+    z = np.stack([oracle.decode_rows(pool[b].numpy(), kv) @ q[b, 0].double().numpy() for b in range(B)]) * SCALE
+    lse = torch.from_numpy(np.log(np.exp(z).sum(1))).float()[:, None]
+    mass = torch.zeros(B, n, device="cuda")
+    ws = _u8(dcpmla.mla_attention_mass_workspace_size(B, 1))
+    dcpmla.mla_attention_mass(q.cuda(), pool.cuda(), kv, table.cuda(), _i32([n] * B), 0, 1, SCALE, lse.cuda(), mass,
+                              ws, 0.0)
+    want = np.exp(z - lse.double().numpy())
+    off = mass.cpu().double().numpy() / want - 1
+    # a weight's relative error is its exponent's error: the scores' and the log-sum's sizes are below 16, so six
+    # fp32 additions and two constants add 2^-25 * 16 each at most, 0.6 of that in the mean square
+    assert np.sqrt((off ** 2).mean()) <= np.sqrt(8) * 0.6 * 16 * 2.0 ** -25
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_summaries_of_many_requests(kv):
     """More requests than one look at the lengths covers; each block belongs to one of them."""
     B = 1500
