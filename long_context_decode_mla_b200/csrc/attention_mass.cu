@@ -40,8 +40,8 @@
 //
 // HBM bounds bf16 rows (per further row 6.9 TB/s; 32 requests of 8,191 rows 58 us
 // with some 15 us of start and ends), the MMAs' issue and HBM together fp8 rows
-// (6.1 TB/s; 779,084 rows 106 us, 125 once back-to-back calls have brought the
-// device to its power limit).
+// (779,084 rows 113 us; more once back-to-back calls have brought the device to its
+// power limit).
 #include "dcpmla.h"
 
 #include <cuda.h>
@@ -64,6 +64,7 @@ struct MassParams {
   float* mass;
   long long mass_stride;
   float decay;
+  float scale2, scale2_err;   // softmax scale * log2(e) in fp32, and its relative rounding
   CUtensorMap rows;      // [blocks][64][row bytes] u8, box 128 x 64, 128-byte swizzle
   CUtensorMap scales;    // fp8: the same, box 16 x 64 (the four fp32 scales)
   CUtensorMap q;         // bf16: [batch][rows][1152] u8, box 128 x 64, rows past the pass zero
@@ -82,7 +83,7 @@ constexpr uint32_t kQBytes = 9 * kHalf;            // fp8: hi, lo, rope; bf16: n
 constexpr int kPrefetchTiles = 1;                  // more crowd the L2: 61 us at 1, 86 at 4
 constexpr int kMaxSeg = 64;
 constexpr int kTileMass = 128;                     // rows of a tile
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.4426950408889634 - (double)kLog2e;
 
 template <int kDtype>
 struct Shape;
@@ -105,7 +106,9 @@ struct Ctl {
   uint64_t d_full[kMaxBufs], d_empty[kMaxBufs];    // an accumulator done / read
   uint64_t meta[kMeta];                      // a tile's row counts written and scales landed
   uint64_t q_full, q_empty;
-  alignas(16) float2 head[64];               // 2^-a scale log2(e), lse log2(e)
+  // fp8: 2^-a; lse log2(e) in fp32; a factor for the weights that makes up for what
+  // the rounding of that and of the scale left, at the weights that matter
+  alignas(16) float4 head[64];
   float half[2][kTileMass];                  // [tile parity]: the other half's sums
   int nv[kMeta][2];                          // rows of each block that take part
   uint32_t tmem_base;
@@ -320,7 +323,7 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
   const uint32_t lane_base =
       c.tmem_base + ((uint32_t)((row >> 5) * 32) << 16) + 32 * hh;
   const int hpq = p.heads / p.q_len;
-  const float sl2 = p.scale * kLog2e;
+  const float sl2 = m.scale2;
   PairCursor cur;
   if (!cur.start(p, c, nseg)) return;
   while (true) {
@@ -329,16 +332,20 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
       // the readers of the old factors passed the last tile's barrier
       if (threadIdx.x < 64) {
         const int h = threadIdx.x;
-        float2 f = make_float2(0.f, INFINITY);     // rows past the pass weigh nothing
+        float4 f = make_float4(0.f, INFINITY, 1.f, 0.f);     // rows past the pass weigh nothing
         if (h < p.heads) {
-          f.x = sl2;
+          f.x = 1.f;
           if constexpr (kDtype == kKvFp8) {
             ptx::wait_primary();
-            f.x *= __ldcg(reinterpret_cast<const float*>(p.q_image + (size_t)b * kQImageBytes +
+            f.x = __ldcg(reinterpret_cast<const float*>(p.q_image + (size_t)b * kQImageBytes +
                                                          kQBytes) + h);
           }
           const float l = __ldg(m.lse + (size_t)b * p.rows_o + h);
+          // A weight near 1 has scale s = lse, and sl2 s - f.y is then off by what both
+          // constants' roundings are: lse log2(e) (1 + err) - f.y, the same for all rows.
           f.y = l == -INFINITY ? INFINITY : l * kLog2e;
+          if (isfinite(f.y))
+            f.z = exp2f(-(fmaf(l, kLog2e, -f.y) + l * kLog2eLo + f.y * m.scale2_err));
         }
         c.head[h] = f;
       }
@@ -394,13 +401,12 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float2 f = c.head[32 * hh + e];
+          const float4 f = c.head[32 * hh + e];
           const float z = __uint_as_float(x[e]);       // the rope
-          const float y = kDtype == kKvFp8 ? fmaf(f.x, v[e], fmaf(sl2, z, -f.y))
-                                           : fmaf(f.x, v[e] + z, -f.y);
-          float w = ex2(y);
+          const float s = kDtype == kKvFp8 ? fmaf(f.x, v[e], z) : v[e] + z;
+          float w = ex2(fmaf(sl2, s, -f.y));
           if (masked && 32 * hh + e < from) w = 0.f;
-          sum += w;
+          sum = fmaf(f.z, w, sum);
         }
       }
     }
@@ -638,6 +644,9 @@ int mla_attention_mass(const void* q, const void* kv_cache, int kv_dtype, int64_
     p.len_delta = q_len - k1;
     m.lse = lse + (size_t)k0 * num_heads;
     m.decay = k1 == q_len ? decay : 1.f;
+    const double scale2 = (double)softmax_scale * 1.4426950408889634;
+    m.scale2 = (float)scale2;
+    m.scale2_err = scale2 != 0. ? (float)(m.scale2 / scale2 - 1.) : 0.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = kv_dtype == DCPMLA_KV_FP8 ? launch_mass<kKvFp8>(m, dev, st)
                                                     : launch_mass<kKvBf16>(m, dev, st);
