@@ -107,7 +107,8 @@ struct Ctl {
   uint64_t meta[kMeta];                      // a tile's row counts written and scales landed
   uint64_t q_full, q_empty;
   // fp8: 2^-a; lse log2(e) in fp32; a factor for the weights that makes up for what
-  // the rounding of that and of the scale left, at the weights that matter
+  // the rounding of that and of the scale left, at the weights that matter; -inf for a
+  // row of Q that weighs nothing whatever its score (fminf prefers it to a NaN), else NaN
   alignas(16) float4 head[64];
   float half[2][kTileMass];                  // [tile parity]: the other half's sums
   int nv[kMeta][2];                          // rows of each block that take part
@@ -332,7 +333,7 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
       // the readers of the old factors passed the last tile's barrier
       if (threadIdx.x < 64) {
         const int h = threadIdx.x;
-        float4 f = make_float4(0.f, INFINITY, 1.f, 0.f);     // rows past the pass weigh nothing
+        float4 f = make_float4(0.f, 0.f, 1.f, -INFINITY);     // rows past the pass weigh nothing
         if (h < p.heads) {
           f.x = 1.f;
           if constexpr (kDtype == kKvFp8) {
@@ -341,11 +342,14 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
                                                          kQBytes) + h);
           }
           const float l = __ldg(m.lse + (size_t)b * p.rows_o + h);
-          // A weight near 1 has scale s = lse, and sl2 s - f.y is then off by what both
-          // constants' roundings are: lse log2(e) (1 + err) - f.y, the same for all rows.
-          f.y = l == -INFINITY ? INFINITY : l * kLog2e;
-          if (isfinite(f.y))
-            f.z = exp2f(-(fmaf(l, kLog2e, -f.y) + l * kLog2eLo + f.y * m.scale2_err));
+          if (l != -INFINITY) {
+            f.y = l * kLog2e;
+            f.w = NAN;
+            // A weight near 1 has scale s = lse, and sl2 s - f.y is then off by what both
+            // constants' roundings are: lse log2(e) (1 + err) - f.y, the same for all rows.
+            if (isfinite(f.y))
+              f.z = exp2f(-(fmaf(l, kLog2e, -f.y) + l * kLog2eLo + f.y * m.scale2_err));
+          }
         }
         c.head[h] = f;
       }
@@ -404,7 +408,7 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
           const float4 f = c.head[32 * hh + e];
           const float z = __uint_as_float(x[e]);       // the rope
           const float s = kDtype == kKvFp8 ? fmaf(f.x, v[e], z) : v[e] + z;
-          float w = ex2(fmaf(sl2, s, -f.y));
+          float w = ex2(fminf(fmaf(sl2, s, -f.y), f.w));
           if (masked && 32 * hh + e < from) w = 0.f;
           sum = fmaf(f.z, w, sum);
         }
