@@ -347,8 +347,12 @@ __device__ __forceinline__ void weight_role(const MassParams& m, Ctl& c, uint8_t
             f.w = NAN;
             // A weight near 1 has scale s = lse, and sl2 s - f.y is then off by what both
             // constants' roundings are: lse log2(e) (1 + err) - f.y, the same for all rows.
-            if (isfinite(f.y))
-              f.z = exp2f(-(fmaf(l, kLog2e, -f.y) + l * kLog2eLo + f.y * m.scale2_err));
+            // At an LSE of 2^22 and more, where fp32 scores are worse than that, it is
+            // held to one: far beyond, an infinite factor would meet weights of zero.
+            if (isfinite(f.y)) {
+              const float off = fmaf(l, kLog2e, -f.y) + l * kLog2eLo + f.y * m.scale2_err;
+              f.z = exp2f(fminf(1.f, fmaxf(-1.f, -off)));
+            }
           }
         }
         c.head[h] = f;

@@ -94,3 +94,15 @@ def test_a_row_of_nan_is_nan_for_those_who_saw_it_only(kv):
     seen = _mass(p, q, kv, torch.full((len(LENS), 1, 4), 4.0), start)
     assert torch.isnan(seen[b, j]) and int(torch.isnan(seen).sum()) == 1
     assert torch.equal(_mass(p, q, kv, torch.full((len(LENS), 1, 4), -np.inf), start), start)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("scale", [SCALE, 0.1, 1.0, -0.07])
+def test_a_log_sum_far_above_the_scores_leaves_nothing(kv, scale):
+    """exp(score - lse) is zero from some 200 on, up to the largest finite log-sum."""
+    p, q = _case(kv, 5, 1)
+    start = torch.rand(len(LENS), 192, generator=torch.Generator().manual_seed(5))
+    # products of 576 values of about 1 stay below 200, so that exp() of these differences underflows
+    for far in (1e3, 3e8, 1.3e9, 7.7e9, 1e12, 3.3e19, 2.2e30, 1.9e38, 3.4e38, np.inf):
+        lse = torch.full((len(LENS), 1, 5), far)
+        assert torch.equal(_mass(p, q, kv, lse, start, scale=scale), start), far
