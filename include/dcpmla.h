@@ -576,7 +576,7 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
  *                entries outside the pool (DCPMLA_FLAG_BAD_BLOCK).
  *   workspace    mla_attention_mass_workspace_size(...) bytes, 16-byte aligned;
  *                its flag word as in mla_decode_workspace_size.
- *   num_splits   CTAs (0: the SM count).
+ *   num_splits   CTAs (0: the SM count; at most one a table entry is launched).
  * The result does not depend on num_splits.
  * Returns DCPMLA_OK or a negative code.
  */

@@ -46,6 +46,7 @@
 
 #include <cuda.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   ptx::tc_fence_after();
   const int T = total_tiles(p, c.warp_sums);
   // an even number of blocks a CTA, so that few tiles are half empty
-  int tpc = T > 0 ? (T + p.num_ctas - 1) / p.num_ctas : 0;
+  int tpc = T > 0 ? (T - 1) / p.num_ctas + 1 : 0;
   tpc += tpc & 1;
   const int lo = min((long long)T, (long long)blockIdx.x * tpc), hi = min(T, lo + tpc);
   Counts n;
@@ -621,6 +622,9 @@ int mla_attention_mass(const void* q, const void* kv_cache, int kv_dtype, int64_
     rc = dcpmla_device_sm_count(&ctas);
     if (rc != DCPMLA_OK) return rc;
   }
+  // no more CTAs than the tables have blocks: any number may be asked for, and
+  // rounding up by more than the tiles there are must not leave the int range
+  ctas = (int)std::min<long long>(ctas, (long long)batch * block_table_stride);
   if (cudaGetDevice(&dev) != cudaSuccess) return DCPMLA_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevicesConfigured) return DCPMLA_ERR_UNSUPPORTED;
   MassParams m{};

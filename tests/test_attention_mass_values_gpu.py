@@ -106,3 +106,13 @@ def test_a_log_sum_far_above_the_scores_leaves_nothing(kv, scale):
     for far in (1e3, 3e8, 1.3e9, 7.7e9, 1e12, 3.3e19, 2.2e30, 1.9e38, 3.4e38, np.inf):
         lse = torch.full((len(LENS), 1, 5), far)
         assert torch.equal(_mass(p, q, kv, lse, start, scale=scale), start), far
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("splits", [6, 149, 1 << 20, (1 << 31) - 1])
+def test_any_number_of_ctas(kv, splits):
+    """More CTAs than tiles, up to the largest int: the same bits as one CTA."""
+    p, q = _case(kv, 7, 2)
+    lse = torch.full((len(LENS), 2, 7), 4.0)
+    start = torch.rand(len(LENS), 192, generator=torch.Generator().manual_seed(6))
+    assert torch.equal(_mass(p, q, kv, lse, start, splits=splits), _mass(p, q, kv, lse, start, splits=1))
