@@ -505,7 +505,8 @@ int mla_block_summary(const void* kv_cache, int kv_dtype, int64_t num_blocks, in
  * in fp32, each operation rounded by itself.  Taken are the first sink_blocks
  * and the last recent_blocks of the request's blocks on this shard, then the
  * highest ranks, ties to the lowest index, block_topk in all (all of them if
- * there are no more).  The choice does not depend on launch shapes.  A summary
+ * there are no more).  The choice does not depend on launch shapes.  It is the
+ * one for a positive softmax scale; for a negative one pass -q.  A summary
  * counts all rows of its block; what a query reads of it ends with what it sees.
  *
  *   q           [batch][q_len][num_heads][576] bf16, 16-byte aligned; query i
@@ -542,9 +543,10 @@ int mla_block_select(const void* q, const void* summaries, int64_t num_blocks, i
  * over the blocks taken (every query token over its own).  Arguments as in
  * those two calls (out_partial [batch][q_len][num_heads][512], out_lse
  * [batch][q_len][num_heads], out_blocks may be NULL); the partials of the
- * shards merge with dcp_merge.  impl is one of DCPMLA_IMPL_* (the test bit is
- * refused).  With block_topk at least the number of blocks this is dense
- * decode.  The flag word is the workspace's first.
+ * shards merge with dcp_merge.  With a negative softmax_scale the blocks are
+ * ranked by -q.  impl is one of DCPMLA_IMPL_* (the test bit is refused).  With
+ * block_topk at least the number of blocks this is dense decode.  The flag word
+ * is the workspace's first.
  * Returns DCPMLA_OK or a negative code.
  */
 int mla_decode_blocks_workspace_size(int batch, int num_heads, int q_len, int block_table_stride,

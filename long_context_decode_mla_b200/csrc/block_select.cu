@@ -3,7 +3,8 @@
 // the chosen blocks.
 //
 //   q codes: per head and scale group, step = max|q| * fp32(1/127) (1 if 0), code
-//            = rint(q / step)                               (values not finite: 0)
+//            = rint(q / step)                               (values not finite: 0;
+//            a decode with a negative softmax scale: the codes of -q)
 //   s_hb   = sum over the five groups, in order, of
 //            fp32(codes_q . codes_b) * (step_hg * scale_bg)  (fp32, no fusing)
 //   rank_b = max_h (s_hb - max_b' s_hb')
@@ -52,6 +53,7 @@ struct SelectParams {
   int tiles;                   // scoring tiles per row (from the table's stride)
   uint8_t* q_codes;            // [rows][kQBytes]
   uint8_t* q_image;            // the e4m3 decode kernel's Q images, or nullptr
+  int negate;                  // 1: rank by -q (a negative softmax scale)
   int num_ctas;                // SMs
   float* scores;               // [rows][tiles][heads][kTile]
   uint32_t* row_max;           // [rows][64] the heads' best scores, as ordered keys
@@ -121,15 +123,16 @@ __global__ void __launch_bounds__(kCodeThreads) q_codes_kernel(const SelectParam
   finite = __reduce_max_sync(lanes, finite);
   const float amax = __uint_as_float(finite);
   const float up = __fmul_rn(amax, kInv127), step = up > 0.f ? up : 1.f;
-  const float inv = __frcp_rn(step);
+  const float by = p.negate ? -step : step;
+  const float inv = __frcp_rn(by);
   uint32_t code[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    // x / step, to the nearest: the product with the reciprocal is within 2^-16 of the
+    // x / by, to the nearest: the product with the reciprocal is within 2^-16 of the
     // quotient (magnitudes up to 127); near a half, or where the reciprocal overflowed,
     // the division decides
     float c = rintf(__fmul_rn(x[e], inv));
-    if (!(fabsf(__fsub_rn(__fmul_rn(x[e], inv), c)) < 0.4999f)) c = rintf(__fdiv_rn(x[e], step));
+    if (!(fabsf(__fsub_rn(__fmul_rn(x[e], inv), c)) < 0.4999f)) c = rintf(__fdiv_rn(x[e], by));
     code[e >> 2] |= ((uint32_t)min(127, max(-127, (int)c)) & 0xFFu) << (8 * (e & 3));
   }
   uint8_t* out = p.q_codes + (size_t)r * kQBytes;
@@ -1000,6 +1003,7 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
   p.out_table = reinterpret_cast<int*>(sel + layout(rows, num_heads, block_table_stride).total);
   p.out_lens = p.out_table + round256((size_t)rows * block_topk * 4) / 4;
   p.flags = static_cast<int*>(workspace);
+  p.negate = softmax_scale < 0.f;
   p.q_image = decode_chosen_q_image(kv_dtype, rows, num_heads, splits, impl, workspace);
   rc = run_select(p, sel, static_cast<cudaStream_t>(stream));
   if (rc != DCPMLA_OK) return rc;
