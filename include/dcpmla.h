@@ -483,7 +483,9 @@ int pcp_prefill_attention(const void* q, const int32_t* positions, int num_queri
  *                    `summaries` is written.
  *   flags            NULL or a DEVICE int32: DCPMLA_FLAG_BAD_BLOCK,
  *                    DCPMLA_FLAG_BAD_LENGTH; such blocks are skipped.
- * Rows past a request's end do not enter the mean, whatever they hold.  A block
+ * Rows past a request's end do not enter the mean, whatever they hold.  A summary
+ * is stale once rows of its block have been written or moved (mla_cache_evict
+ * moves rows into any of a request's blocks).  A block
  * that several requests share has to hold the same rows for all of them (a
  * common prefix of whole blocks does): else its summary is undefined.
  * Returns DCPMLA_OK or a negative code.
@@ -572,8 +574,9 @@ int mla_decode_blocks(const void* q, const void* kv_cache, int kv_dtype, const v
  *   lse          [batch][q_len][num_heads] fp32 natural-log LSE (-inf: the query
  *                saw nothing and adds nothing).
  *   decay        finite, >= 0; 0: the old mass is not read (it may be anything).
- *   mass         [batch][mass_stride] fp32, in local row order; nothing past a
- *                request's rows is touched.  Rows beyond mass_stride are flagged
+ *   mass         [batch][mass_stride] fp32, in local row order; a new row's entry
+ *                has to be 0 before its first call (unless decay is 0).  Nothing
+ *                past a request's rows is touched.  Rows beyond mass_stride are flagged
  *                (DCPMLA_FLAG_BAD_LENGTH) and skipped; so are the rows of table
  *                entries outside the pool (DCPMLA_FLAG_BAD_BLOCK).
  *   workspace    mla_attention_mass_workspace_size(...) bytes, 16-byte aligned;
@@ -600,9 +603,21 @@ int mla_attention_mass(const void* q, const void* kv_cache, int kv_dtype, int64_
  * the budget stays where it is; the kept rows at or past it fill, in order, the
  * places below it that were given up.  Rows 0 .. rows_out[b]-1 are then the
  * request's cache; the blocks past them are free.  Attention does not depend on
- * the order of the rows, but they are no longer in token order: decode them as
- * one shard of their own (shard_id 0, num_shards 1, seq_lens = rows_out), and
- * append at local row rows_out[b] in the same way.
+ * the order of the rows, but they are no longer in token order.
+ *
+ * An evicted cache in use, from then on:
+ *  - It is decoded, weighed and appended to as one shard of its own: shard_id 0,
+ *    num_shards 1, seq_lens = the rows held; a token this shard owns is appended
+ *    at that local row.
+ *  - Its summaries are stale, the blocks below the budget among them: write all
+ *    of the request's again (mla_block_summary without first_positions) before
+ *    blocks are chosen by them.  After that first_positions = the first appended
+ *    local row keeps them current.
+ *  - mass and positions of an appended row are the caller's to set, before it is
+ *    weighed or evicted: mass 0 and the row's token.  What the arrays hold there
+ *    is left from before (in place: a row given up).
+ *  - The next eviction takes `rows` = the rows held and `positions`, still with
+ *    global seq_lens and this shard's shard_id and num_shards.
  *
  *   seq_lens      [batch] int32 GLOBAL lengths L_b (for `recent`).
  *   rows          NULL before the first eviction (the shard's share of L_b), else
@@ -610,9 +625,10 @@ int mla_attention_mass(const void* q, const void* kv_cache, int kv_dtype, int64_
  *   mass          [batch][mass_stride] fp32.
  *   positions     NULL before the first eviction (row j is token j * num_shards
  *                 + shard_id), else [batch][mass_stride] int32 token of each row.
- *   mass_out, positions_out  the kept rows' entries in their new order, the rest
- *                 untouched; each may be the input array itself (no other
- *                 overlap).  positions_out may be NULL.
+ *   mass_out, positions_out  the kept rows' entries in their new order; from
+ *                 rows_out[b] on untouched and without meaning.  Each may be the
+ *                 input array itself (no other overlap).  positions_out may be
+ *                 NULL.
  *   rows_out      [batch] int32, not `rows` nor `seq_lens`.
  *   kv_cache      rows are moved within each request's blocks: no block written
  *                 to may be shared with another request.

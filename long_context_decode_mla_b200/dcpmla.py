@@ -536,7 +536,7 @@ def mla_attention_mass(q, kv_cache, kv_dtype, block_table, seq_lens, shard_id, n
                        num_blocks: int | None = None):
     """Adds this step's attention weight to ``mass`` [B, rows] (see
     include/dcpmla.h): q [B, H, 576] or [B, q_len, H, 576], lse the (merged)
-    LSE of the same queries and heads."""
+    LSE of the same queries and heads.  A new row's entry starts at 0."""
     B, Q, H = _query_shape(q)
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
     kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
@@ -562,7 +562,12 @@ def mla_cache_evict(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_sha
                     num_blocks: int | None = None):
     """Keeps the ``budget`` rows of largest mass of every request, in place (see
     include/dcpmla.h).  mass, mass_out fp32 and positions, positions_out int32
-    are [B, rows]; an output may be the input itself."""
+    are [B, rows]; an output may be the input itself.
+
+    The cache is then one shard of its own (shard 0 of 1) of ``rows_out`` rows:
+    all of its summaries have to be written again, and a row appended at
+    ``rows_out`` gets mass 0 and its token's position before it is weighed
+    (``mass.scatter_(1, rows_out[:, None].long(), 0)``, the positions alike)."""
     B = seq_lens.shape[0]
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
     kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)
