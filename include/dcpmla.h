@@ -609,6 +609,13 @@ int mla_attention_mass(const void* q, const void* kv_cache, int kv_dtype, int64_
  *  - It is decoded, weighed and appended to as one shard of its own: shard_id 0,
  *    num_shards 1, seq_lens = the rows held; a token this shard owns is appended
  *    at that local row.
+ *  - With q_len > 1 that form hides the last q_len - 1 - i rows from query i, as
+ *    though the shard held all of the step's tokens: right for one shard only.
+ *    Over several shards pass every (request, query) as a request of its own
+ *    (q_len 1, the request's table row again), seq_lens = the rows held before the
+ *    step plus the step's tokens up to that query which this shard owns.
+ *    mla_attention_mass: a call per query i with those lengths, the last query
+ *    first, with the decay, and the others with decay 1.
  *  - Its summaries are stale, the blocks below the budget among them: write all
  *    of the request's again (mla_block_summary without first_positions) before
  *    blocks are chosen by them.  After that first_positions = the first appended

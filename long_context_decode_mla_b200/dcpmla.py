@@ -567,7 +567,9 @@ def mla_cache_evict(kv_cache, kv_dtype, block_table, seq_lens, shard_id, num_sha
     The cache is then one shard of its own (shard 0 of 1) of ``rows_out`` rows:
     all of its summaries have to be written again, and a row appended at
     ``rows_out`` gets mass 0 and its token's position before it is weighed
-    (``mass.scatter_(1, rows_out[:, None].long(), 0)``, the positions alike)."""
+    (``mass.scatter_(1, rows_out[:, None].long(), 0)``, the positions alike).
+    Of several shards it takes one query token a request: draft tokens are
+    requests of their own there, each with its own length (see the header)."""
     B = seq_lens.shape[0]
     nb = kv_cache.shape[0] if num_blocks is None else num_blocks
     kvd = _expect_cache(kv_cache, kv_dtype, nb, block_size)

@@ -1,5 +1,6 @@
 """Evicted caches that go on being used: tokens appended behind the kept rows,
-summaries, choice, decode, weights and further evictions in place.
+summaries, choice, decode, weights and further evictions in place, and draft
+tokens over shards that no longer hold their share of the positions.
 
 What the calls leave to the caller is done here as the header states it: after
 an eviction every summary of the request is written again, and an appended row
@@ -175,3 +176,90 @@ def test_evicted_caches_are_appended_to_weighed_and_evicted_again(kv, N):
                 c.err[s] = decay * c.err[s] + e
         c.summaries_are_current()
     assert _flag(dws) == 0 and _flag(mws) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("N", [1, 2, 3])
+def test_draft_tokens_over_evicted_shards(kv, N):
+    """Each (request, draft) is a request of its own, of as many rows as that draft sees on the shard: the kept
+    ones and the drafts up to it that the shard owns."""
+    H, Q, topk, decay = 8, 3, 2, 0.5
+    c = _Caches(kv, N, H, [700, 66, 401], 8, 5)
+    B = c.B
+    c.evict(150, 2, 20)
+    held = [r.clone() for r in c.rows]
+    first = c.lens.copy()
+    for _ in range(Q):
+        c.append()
+    q = torch.randn(B, Q, H, 576, generator=c.g).to(torch.bfloat16)
+    flat = q.view(B * Q, H, 576).cuda()
+    lens, tables = [], []
+    for s in range(N):
+        t = _i32(first)[:, None] + torch.arange(Q, device="cuda", dtype=torch.int32)[None]
+        lens.append((held[s][:, None] + torch.cumsum(t % N == s, 1)).to(torch.int32).contiguous())      # [B, Q]
+        tables.append(c.t[s].repeat_interleave(Q, 0).contiguous())
+        for b in range(B):
+            for i in range(Q):
+                assert np.array_equal(c.seen(s, b, Q, i), np.arange(int(lens[s][b, i])))
+    R = B * Q
+    parts, lses = torch.empty(N, R, H, 512, device="cuda"), torch.empty(N, R, H, device="cuda")
+    out, lse = torch.empty(R, H, 512, device="cuda"), torch.empty(R, H, device="cuda")
+    ws = _ws(dcpmla.mla_decode_workspace_size(R, H))
+    bws = _ws(dcpmla.mla_decode_blocks_workspace_size(R, H, 1, c.stride, topk))
+    blocks = torch.empty(R, topk, dtype=torch.int32, device="cuda")
+    for chosen in (True, False):
+        o64, l64 = np.zeros((N, R, H, 512)), np.full((N, R, H), -np.inf)
+        for s in range(N):
+            n = lens[s].view(R)
+            if chosen:
+                dcpmla.mla_decode_blocks(flat, c.cache, kv, c.S, tables[s], n, 0, 1, topk, SCALE, parts[s], lses[s], bws,
+                                         blocks)
+                want, _ = ob.block_select(_bits(q).reshape(R, 1, H, 576), c.S.cpu().numpy(), tables[s].cpu().numpy(),
+                                          n.cpu().numpy(), 0, 1, topk, 1, 1)
+                assert np.array_equal(blocks.cpu().numpy(), want[:, 0])
+            else:
+                dcpmla.mla_decode_partial(flat, c.cache, kv, tables[s], n, 0, 1, None, SCALE, parts[s], lses[s], ws)
+            for b in range(B):
+                for i in range(Q):
+                    seen = c.seen(s, b, Q, i)
+                    if chosen:
+                        seen = seen[np.isin(seen // 64, want[b * Q + i, 0])]
+                    o64[s, b * Q + i], l64[s, b * Q + i] = oracle.attention_with_lse(
+                        oracle.decode_bf16(_bits(q)[b, i]), c.values(s, b)[seen], SCALE)
+        dcpmla.dcp_merge(parts, lses, out, lse)
+        c.check(out, lse, *oracle.dcp_merge(o64, l64))
+    # the weights: a call a draft, the newest first (it sees every row, so its call carries the decay)
+    mws = _ws(dcpmla.mla_attention_mass_workspace_size(B, H))
+    wl64 = lse.view(B, Q, H).double().cpu().numpy()
+    for s in range(N):
+        for i in reversed(range(Q)):
+            d = decay if i == Q - 1 else 1.0
+            dcpmla.mla_attention_mass(q[:, i].contiguous().cuda(), c.cache, kv, c.t[s], lens[s][:, i].contiguous(), 0, 1,
+                                      SCALE, lse.view(B, Q, H)[:, i].contiguous(), c.mass[s], mws, d)
+        got = c.mass[s].double().cpu().numpy()
+        for b in range(B):
+            n, k = c.ref_rows[s][b], c.values(s, b)
+            want, err = decay * c.want[s][b, :n], np.zeros(n)
+            for i in range(Q):
+                see = np.zeros(n, bool)
+                see[c.seen(s, b, Q, i)] = True
+                qi = oracle.decode_bf16(_bits(q)[b, i])
+                z = SCALE * (qi @ k.T)
+                w = np.where(see, np.exp(z - wl64[b, i][:, None]), 0.0)
+                # as in the oracle of the weights: 576 exact products summed in fp32, small values of q cut at 2^-17
+                # of the largest in fp8, then the scale, a difference and the exponential
+                e = 576 * 2.0 ** -24 * SCALE * (np.abs(qi) @ np.abs(k).T) + 2.0 ** -22 * (np.abs(z)
+                                                                                         + np.abs(wl64[b, i][:, None]) + 1)
+                if kv == "fp8":
+                    e += SCALE * np.abs(k).sum(1) * np.abs(qi).max(1, keepdims=True) * 2.0 ** -17
+                want += w.sum(0)
+                err += (w * e).sum(0)
+            err += 2.0 ** -23 * (want + 1)
+            assert (np.abs(got[b, :n] - want) <= err).all()
+    if N == 1:
+        # one shard holds every draft: the batched form sees the same
+        mo, ml = torch.empty(B, Q * H, 512, device="cuda"), torch.empty(B, Q * H, device="cuda")
+        dcpmla.mla_decode_partial_multi(q.cuda(), c.cache, kv, c.t[0], c.rows[0], 0, 1, SCALE, mo, ml,
+                                        _ws(dcpmla.mla_decode_workspace_size(B, Q * H)))
+        c.check(mo.view(R, H, 512), ml.view(R, H), *oracle.dcp_merge(o64, l64))
+    assert _flag(ws) == 0 and _flag(bws) == 0 and _flag(mws) == 0
