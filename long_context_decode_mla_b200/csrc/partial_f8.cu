@@ -33,13 +33,14 @@
 //    for group g, P_g = p * s_tg * (8 / S_g), stored as two e4m3 terms (hi:
 //    the 4 leading bits of the fp16 value, lo: the rest rounded to 4 bits;
 //    together within max(2^-7 P_g, 2^-9) of P_g) in a 64 x 64 K-major tile
-//    per term; the two
-//    PV MMAs of a term pair share V through a collector buffer.  S_g is a
+//    per term; the two PV MMAs of a term pair share V through a collector
+//    buffer.  Chosen blocks: p * s_tg * (28 / S_g) with hi rounded, within
+//    max(2^-9 P_g, 2^-10) from 2^-6 on (2^-9 below).  S_g is a
 //    per-request reference scale (the group's largest scale in the request's
 //    first tile, raised with an exact O rescale if a later tile holds a scale
-//    more than 4x larger), so P_g stays below 256 and the tokens that carry
-//    the softmax mass stay in the e4m3 normal range; the epilogue multiplies
-//    O_g back by S_g / 8.
+//    more than 4x larger; chosen blocks: 2x), so P_g stays below 256 (448) and
+//    the tokens that carry the softmax mass stay in the e4m3 normal range; the
+//    epilogue multiplies O_g back by S_g / 8 (28).
 //  * O (64 heads x 512, fp32) stays in TMEM for the whole request, in the
 //    weight-stationary M = 64 layout (one N = 128 accumulator per group).
 //
@@ -134,8 +135,18 @@ constexpr int kMaxSegF8 = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 3.f;     // lazy max: rescale O when the max grows by > 2^3
-constexpr float kPNorm = 8.f;           // P_g = p * s * (kPNorm / S_g)
-constexpr float kScaleSlack = 4.f;      // a tile scale up to 4 S_g needs no rescale
+// P_g = p * s * (norm / S_g), and a tile scale up to `slack` times S_g needs no
+// rescale: with p up to 2^3, P_g stays within 256.  A choice of a few thousand rows
+// holds many that weigh little each, and what e4m3 cuts off below its smallest step
+// adds up over them (4,000 rows of a choice: 2.0e-3 of O at norm 8): there P_g takes
+// all of the format's range, up to 448.
+template <bool kChosen>
+constexpr float kPNorm = kChosen ? 28.f : 8.f;
+template <bool kChosen>
+constexpr float kScaleSlack = kChosen ? 2.f : 4.f;
+static_assert(kPNorm<false> * kScaleSlack<false> * 8.f <= 448.f &&
+                  kPNorm<true> * kScaleSlack<true> * 8.f <= 448.f,
+              "P_g within e4m3");
 constexpr int kFlagTimeout = 4;
 
 // collector buffer of the PV issuer (the score MMAs gain nothing from one)
@@ -152,7 +163,7 @@ struct F8Params {
 
 struct F8Ctl {
   alignas(16) float sT[2][4][64];   // a tile's scales, [tile parity][group][row]
-  alignas(16) __half sTp[2][4][64]; // the same times kPNorm / S_g (fp16), 0 for absent rows
+  alignas(16) __half sTp[2][4][64]; // the same times norm / S_g (fp16), 0 for absent rows
   alignas(16) float sc_r[2][4];     // per group: O rescale factor S_old / S_new at this tile
   alignas(16) float sc_ref[2][4];   // per group: S_g in force for this tile
   alignas(16) float gw[2][4][4];    // staging: per-warp group maxima of |scale|
@@ -557,12 +568,12 @@ __device__ __forceinline__ bool listed_fetch(const PartialParams& p, F8Ctl& c, u
 }
 
 // Staging (4 warps): per request, its Q; per tile, once its bytes landed,
-// the scales as [group][row] copies (raw, and times kPNorm / S_g as fp16),
+// the scales as [group][row] copies (raw, and times norm / S_g as fp16),
 // the reference scales S_g with the O rescale factor a raised reference
 // implies, and zeros over the codes of rows past the request's end (their
 // bytes are whatever the block holds and must not reach PV).  Thread u
 // handles row u / 2, groups 2 (u % 2) and 2 (u % 2) + 1.
-template <bool kListed>
+template <bool kListed, bool kChosen>
 __device__ __forceinline__ void staging_role(const PartialParams& p, F8Ctl& c, uint8_t* base, int nseg,
                              uint32_t& tau, uint32_t& sigma) {
   const int u = threadIdx.x - kStageWarp0 * 32;   // 0..127
@@ -619,7 +630,7 @@ __device__ __forceinline__ void staging_role(const PartialParams& p, F8Ctl& c, u
     for (int g = 0; g < 4; ++g) {
       if (first) {
         sref[g] = gm[g] > 0.f ? gm[g] : 1.f;
-      } else if (gm[g] > kScaleSlack * sref[g]) {
+      } else if (gm[g] > kScaleSlack<kChosen> * sref[g]) {
         r[g] = sref[g] / gm[g];
         sref[g] = gm[g];
       }
@@ -631,9 +642,9 @@ __device__ __forceinline__ void staging_role(const PartialParams& p, F8Ctl& c, u
     const float ref0 = gp == 0 ? sref[0] : sref[2], ref1 = gp == 0 ? sref[1] : sref[3];
     c.sT[b][gp][row] = sv.x;
     c.sT[b][gp + 1][row] = sv.y;
-    reinterpret_cast<uint16_t*>(c.sTp[b][gp])[row] = f16_sat(valid ? sv.x * (kPNorm / ref0) : 0.f);
+    reinterpret_cast<uint16_t*>(c.sTp[b][gp])[row] = f16_sat(valid ? sv.x * (kPNorm<kChosen> / ref0) : 0.f);
     reinterpret_cast<uint16_t*>(c.sTp[b][gp + 1])[row] =
-        f16_sat(valid ? sv.y * (kPNorm / ref1) : 0.f);
+        f16_sat(valid ? sv.y * (kPNorm<kChosen> / ref1) : 0.f);
     if (nv < kTileRows) {
       for (int k = u; k < (kTileRows - nv) * 32; k += kStageThreads) {
         const int rr = nv + k / 32, g = (k & 31) >> 3, un = k & 7;
@@ -885,7 +896,7 @@ __device__ __forceinline__ void softmax_role(const PartialParams& p, F8Ctl& c, u
 #pragma unroll 1
       for (int g = 0; g < 4; ++g) {
         const float sg = g == 0 ? sref.x : g == 1 ? sref.y : g == 2 ? sref.z : sref.w;
-        const float f = il * (sg * (1.f / kPNorm));
+        const float f = il * (sg * (1.f / kPNorm<kChosen>));
         uint32_t v32[32];
         ptx::tmem_ld32(lane_base + 64 * g + 32 * th, v32);
         ptx::tmem_wait_ld();
@@ -944,7 +955,7 @@ __device__ __forceinline__ void run_roles(const F8Params& P, const PartialParams
       } else if (warp == kPvWarp) {
         if ((threadIdx.x & 31) == 0) pv_role<kListed>(p, c, base, nseg, tau, uses, o_commits);
       } else {
-        staging_role<kListed>(p, c, base, nseg, tau, sigma);
+        staging_role<kListed, kChosen>(p, c, base, nseg, tau, sigma);
       }
     }
     block_bar();

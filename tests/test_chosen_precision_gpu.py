@@ -128,6 +128,44 @@ def test_fp8_rows_round_the_leading_term_of_p():
     assert np.sqrt(got / total) <= np.sqrt(cut * rounded), (np.sqrt(got / total), cut, rounded)
 
 
+@pytest.mark.parametrize("rows", [4032, 1000])
+def test_fp8_rows_that_weigh_little_are_not_lost(rows):
+    """A choice of thousands of rows: what e4m3 cuts off below its smallest step adds up over them.  The RMS error
+    lies below the geometric mean of what P in a frame of 28 and in one of 8 leaves, with the running maximum as
+    one CTA moves it."""
+    B, H = 4, 8
+    p = wl.make_problem("agentic", num_shards=1, batch=B, heads=H, seq_len=[rows] * B, seed=77)
+    ni = p.numpy_inputs()
+    out, _, _ = _decode(p, "fp8", -(-rows // 64), 1)
+    err, total, got = {28.0: 0.0, 8.0: 0.0}, 0.0, 0.0
+    for b in range(B):
+        k, _ = ob.shard_rows(ni["kv_cache"], "fp8", ni["block_tables"][0, b], rows, 1, 0)
+        raw = p.kv_cache[p.block_tables[0, b].long()].view(-1, 656)[:rows]
+        sc = raw[:, 512:528].contiguous().view(torch.float32)
+        codes = raw[:, :512].contiguous().view(torch.float8_e4m3fn).double()
+        q = oracle.decode_bf16(ni["q"][b])
+        want, lse = oracle.attention_with_lse(q, k, SCALE)
+        s = SCALE / np.log(2.0) * (q @ k.T)
+        used, m = np.empty_like(s), np.full(H, -np.inf)
+        for t in range(0, rows, 64):
+            top = s[:, t:t + 64].max(1)
+            m = np.where(top > m + 3.0, top, m)
+            used[:, t:t + 64] = m[:, None]
+        w = torch.from_numpy(np.exp2(s - used)).half().float()
+        back = torch.from_numpy(np.exp2(used - lse[:, None] / np.log(2.0)))
+        for g in range(4):
+            ref, cols = sc[:64, g].max(), slice(128 * g, 128 * g + 128)
+            for norm in err:
+                p16 = (w * (sc[:, g] * (norm / ref)).half().float()).half()
+                o = ((_p_terms(p16, True).double() * back) @ codes[:, cols]) * (ref / norm)
+                err[norm] += float(((o - torch.from_numpy(want[:, cols])) ** 2).sum())
+        total += (want ** 2).sum()
+        got += ((out[b] - want) ** 2).sum()
+    fine, coarse = np.sqrt(err[28.0] / total), np.sqrt(err[8.0] / total)
+    assert coarse > 1.3 * fine
+    assert np.sqrt(got / total) <= np.sqrt(fine * coarse), (np.sqrt(got / total), fine, coarse)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_a_call_repeats_itself(kv):
     """The same call gives the same bits, whatever the order in which its CTAs run."""
