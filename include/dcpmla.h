@@ -524,7 +524,9 @@ int mla_block_summary(const void* kv_cache, int kv_dtype, int64_t num_blocks, in
  *               mla_decode_partial reads as one shard of batch * q_len requests
  *               (shard_id 0, num_shards 1).
  *   out_lens    [batch][q_len] int32: rows in the blocks taken.
- *   workspace   mla_block_select_workspace_size(...) bytes, 16-byte aligned;
+ *   workspace   mla_block_select_workspace_size(...) bytes, 16-byte aligned
+ *               (43 KB a query, and 4 bytes a query, head and table entry: 64
+ *               queries of 64 heads over tables of 16,384 entries 275 MB);
  *               its flag word as in mla_decode_workspace_size.  Calls that may
  *               overlap on the device (other streams, other graphs) need a
  *               workspace each; so with every call below.
@@ -548,7 +550,9 @@ int mla_block_select(const void* q, const void* summaries, int64_t num_blocks, i
  * shards merge with dcp_merge.  With a negative softmax_scale the blocks are
  * ranked by -q.  impl is one of DCPMLA_IMPL_* (the test bit is refused).  With
  * block_topk at least the number of blocks this is dense decode.  The flag word
- * is the workspace's first.
+ * is the workspace's first.  With AUTO and TC the probabilities are two bf16 terms
+ * for bf16 rows (O within some 1e-5 of its size) and two e4m3 terms for fp8 rows
+ * (6e-4 to 9e-4 RMS); SIMT keeps them in fp32.
  * Returns DCPMLA_OK or a negative code.
  */
 int mla_decode_blocks_workspace_size(int batch, int num_heads, int q_len, int block_table_stride,

@@ -31,17 +31,18 @@
 // long, and 36 of them more than a block's share of HBM time).  Its rows go
 // through a ring of eight 16 KB slots, 128 bytes of every row each, loaded by
 // TMA and given back slot by slot, with whole blocks prefetched into L2 ahead.
-// Warp 8 loads; warps 9 and 10 issue the MMAs (36 a tile); warps 0-3 and 4-7 add each
-// part into the scores of 32 heads a thread, so that a part's accumulator is
-// free again as soon as it is read, and exchange the sums of their halves.
+// Warp 8 loads; warps 9 and 10 issue the MMAs (a tile of bf16 rows 36, of fp8 rows
+// 20: both terms of a group are one operand); warps 0-3 and 4-7 add each part into the
+// scores of 32 heads a thread, so that a part's accumulator is free again as soon as
+// it is read, and exchange the sums of their halves.
 // Tiles are dealt to the CTAs as in decode.  Each row is summed by the same
 // threads in the same order whatever the number of CTAs: no atomics, the same
 // bits every time.  Every wait is bounded.
 //
 // HBM bounds bf16 rows (per further row 6.9 TB/s; 32 requests of 8,191 rows 58 us
 // with some 15 us of start and ends), the MMAs' issue and HBM together fp8 rows
-// (779,084 rows 113 us; more once back-to-back calls have brought the device to its
-// power limit).
+// (779,084 rows 115 us; 130 to 138 once back-to-back calls have brought the device to
+// its power limit).
 #include "dcpmla.h"
 
 #include <cuda.h>

@@ -791,7 +791,9 @@ cudaError_t prepare_device(int dev) {
                                        208 * 1024);
   if (e != cudaSuccess) return e;
   // the register split assumes exactly kLaunchRegs a thread at launch: with fewer the
-  // scoring warpgroups' increase could never be granted
+  // scoring warpgroups' increase could never be granted.  A kernel that moves registers
+  // is launched with as many as its launch bounds leave a thread (65,536 / 512),
+  // whatever its code needs; this check is for a compiler that does otherwise
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, score_kernel);
   if (e != cudaSuccess) return e;
