@@ -552,7 +552,9 @@ int mla_block_select(const void* q, const void* summaries, int64_t num_blocks, i
  * block_topk at least the number of blocks this is dense decode.  The flag word
  * is the workspace's first.  With AUTO and TC the probabilities are two bf16 terms
  * for bf16 rows (O within some 1e-5 of its size) and two e4m3 terms for fp8 rows
- * (6e-4 to 9e-4 RMS); SIMT keeps them in fp32.
+ * (6e-4 to 9e-4 RMS; more where a row's scale is far above those of the rows that
+ * weigh, beside it: 1.2e-3 at 8 times, 7e-3 at 64 in every block); SIMT keeps them
+ * in fp32.
  * Returns DCPMLA_OK or a negative code.
  */
 int mla_decode_blocks_workspace_size(int batch, int num_heads, int q_len, int block_table_stride,

@@ -128,16 +128,21 @@ def test_fp8_rows_round_the_leading_term_of_p():
     assert np.sqrt(got / total) <= np.sqrt(cut * rounded), (np.sqrt(got / total), cut, rounded)
 
 
-@pytest.mark.parametrize("rows", [4032, 1000])
-def test_fp8_rows_that_weigh_little_are_not_lost(rows):
+@pytest.mark.parametrize("rows,factors", [(4032, (1,)), (1000, (1,)), (4032, (1, 3)), (2050, (1, 3, 9, 27)),
+                                          (2050, (27, 9, 3, 1)), (3000, (1, 1.9, 0.2))])
+def test_fp8_rows_that_weigh_little_are_not_lost(rows, factors):
     """A choice of thousands of rows: what e4m3 cuts off below its smallest step adds up over them.  The RMS error
     lies below the geometric mean of what P in a frame of 28 and in one of 8 leaves, with the running maximum as
-    one CTA moves it."""
+    one CTA moves it and the scales' reference as the blocks' scales (times the factors in turn) raise it."""
     B, H = 4, 8
     p = wl.make_problem("agentic", num_shards=1, batch=B, heads=H, seq_len=[rows] * B, seed=77)
+    for b in range(B):
+        for t in range(-(-rows // 64)):
+            sc = p.kv_cache[int(p.block_tables[0, b, t]), :, 512:528]
+            sc.copy_((sc.contiguous().view(torch.float32) * factors[t % len(factors)]).view(torch.uint8))
     ni = p.numpy_inputs()
     out, _, _ = _decode(p, "fp8", -(-rows // 64), 1)
-    err, total, got = {28.0: 0.0, 8.0: 0.0}, 0.0, 0.0
+    err, total, got = {(28.0, 2.0): 0.0, (8.0, 4.0): 0.0}, 0.0, 0.0
     for b in range(B):
         k, _ = ob.shard_rows(ni["kv_cache"], "fp8", ni["block_tables"][0, b], rows, 1, 0)
         raw = p.kv_cache[p.block_tables[0, b].long()].view(-1, 656)[:rows]
@@ -154,16 +159,24 @@ def test_fp8_rows_that_weigh_little_are_not_lost(rows):
         w = torch.from_numpy(np.exp2(s - used)).half().float()
         back = torch.from_numpy(np.exp2(used - lse[:, None] / np.log(2.0)))
         for g in range(4):
-            ref, cols = sc[:64, g].max(), slice(128 * g, 128 * g + 128)
-            for norm in err:
+            cols = slice(128 * g, 128 * g + 128)
+            for norm, slack in err:
+                ref, r = torch.empty(rows), 0.0
+                for t in range(0, rows, 64):
+                    top = float(sc[t:t + 64, g].max())
+                    r = top if top > slack * r else r
+                    ref[t:t + 64] = r
                 p16 = (w * (sc[:, g] * (norm / ref)).half().float()).half()
-                o = ((_p_terms(p16, True).double() * back) @ codes[:, cols]) * (ref / norm)
-                err[norm] += float(((o - torch.from_numpy(want[:, cols])) ** 2).sum())
+                o = (_p_terms(p16, True).double() * back * (ref / norm)) @ codes[:, cols]
+                err[norm, slack] += float(((o - torch.from_numpy(want[:, cols])) ** 2).sum())
         total += (want ** 2).sum()
         got += ((out[b] - want) ** 2).sum()
-    fine, coarse = np.sqrt(err[28.0] / total), np.sqrt(err[8.0] / total)
-    assert coarse > 1.3 * fine
-    assert np.sqrt(got / total) <= np.sqrt(fine * coarse), (np.sqrt(got / total), fine, coarse)
+    fine, coarse = np.sqrt(err[28.0, 2.0] / total), np.sqrt(err[8.0, 4.0] / total)
+    # few rows carry a softmax of large scores, and then the frames differ little: there the model alone, with scores
+    # up to 3e-4 off (36 additions that cut 2^-23 of sums up to 27 * 17, times the scale, twice)
+    limit = np.sqrt(fine * coarse) if coarse > 1.2 * fine else np.hypot(fine, 3e-4)
+    assert coarse > 1.2 * fine or max(factors) > 1
+    assert np.sqrt(got / total) <= limit, (np.sqrt(got / total), fine, coarse)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
